@@ -14,7 +14,8 @@ own = False
 D = 128            # head dimension of the 4-bit store
 ROWS = 16          # tokens of a group, one page of the store
 BLOCK = 16         # elements that share a scale
-PAGE = ROWS * (D // 2 + D // BLOCK)  # bytes of a page: codes, then scales
+TILE = 32          # elements of a row whose codes lie together: 16 bytes
+PAGE = ROWS * (D // 2 + D // BLOCK)  # bytes of a page: 4 tiles of 16 rows of codes, then 16 rows of scales
 GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
@@ -217,9 +218,11 @@ def _pack(x, ts):
     for b in range(B):
         code, scale = _quantise(x[b], ts)
         code, scale = code[..., 0::2] | (code[..., 1::2] << 4), scale.view(torch.uint8)
-        pad = (0, 0, 0, -n % ROWS)
-        pages[b, :, :, :ROWS * D // 2] = torch.nn.functional.pad(code, pad).reshape(H, -1, ROWS * D // 2)
-        pages[b, :, :, ROWS * D // 2:] = torch.nn.functional.pad(scale, pad).reshape(H, -1, ROWS * D // BLOCK)
+        code, scale = (torch.nn.functional.pad(t, (0, 0, 0, -n % ROWS)).unflatten(1, (-1, ROWS))
+                       for t in (code, scale))
+        code = code.unflatten(-1, (D // TILE, TILE // 2)).transpose(2, 3)  # tile, row, bytes
+        pages[b, :, :, :ROWS * D // 2] = code.flatten(2)
+        pages[b, :, :, ROWS * D // 2:] = scale.flatten(2)
     return pages
 
 
@@ -385,7 +388,8 @@ def _read(pages, group):
     h = torch.arange(H, device="cuda").view(1, -1, 1, 1)
     page = pages[b, h, group.clamp(0, pages.shape[2] - 1)]
     byte, scale = page[..., :ROWS * D // 2], page[..., ROWS * D // 2:]
-    code = torch.stack((byte & 15, byte >> 4), -1).flatten(-2).unflatten(-1, (ROWS, D))
+    byte = byte.unflatten(-1, (D // TILE, ROWS, TILE // 2)).transpose(-3, -2).flatten(-2)
+    code = torch.stack((byte & 15, byte >> 4), -1).flatten(-2)
     return _values(code, scale.view(torch.float8_e4m3fn).unflatten(-1, (ROWS, -1)))
 
 
@@ -475,7 +479,8 @@ def _exact_store(x, ts):
 def _exact_pages(pages, ts):
     """A store's rows [B, H, tokens, D] in 64 bits, from its bits."""
     B, H, n, _ = pages.shape
-    byte = pages[..., :ROWS * D // 2].reshape(B, H, n * ROWS, D // 2).int()
+    byte = pages[..., :ROWS * D // 2].reshape(B, H, n, 4, ROWS, 16)
+    byte = byte.permute(0, 1, 2, 4, 3, 5).reshape(B, H, n * ROWS, D // 2).int()
     sc = pages[..., ROWS * D // 2:].reshape(B, H, n * ROWS, D // BLOCK).int()
     code = torch.stack((byte % 16, byte // 16), -1).reshape(B, H, n * ROWS, D)
     m, e = (code % 8) % 2, (code % 8) // 2
