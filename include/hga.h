@@ -126,8 +126,31 @@ typedef enum { HGA_SUMMARY_F32 = 0, HGA_SUMMARY_BF16 = 1 } hga_summary_type;
  *                  hga_decode_step_tiered) and moved by the gathers
  *                  (hga_gather_kv, hga_gather_kv_warm[_noalloc]). Prefill
  *                  attention (q_len > 1) and a rotated-key output of
- *                  hga_build_summaries return HGA_ERR_UNSUPPORTED. */
-typedef enum { HGA_KV_AS_DTYPE = 0, HGA_KV_E4M3 = 1 } hga_kv_type;
+ *                  hga_build_summaries return HGA_ERR_UNSUPPORTED.
+ * HGA_KV_E2M1:     four bits per element. An element's code is an E2M1
+ *                  number (bit 3 sign, bits 2..1 exponent with bias 1, bit 0
+ *                  mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6); the 16 elements
+ *                  16s .. 16s + 15 of a row share an E4M3 scale code, and the
+ *                  tensor the scale cfg->k_scale (keys) or cfg->v_scale
+ *                  (values): value = code x block scale x tensor scale. The
+ *                  store is made of pages, one per group of 16 tokens
+ *                  (HGA_E2M1_PAGE = 1152 bytes): four tiles of 32 elements,
+ *                  each 16 rows x 16 bytes of codes (element 2i in the low
+ *                  half of byte i), then 16 rows x 8 scale codes. Where the
+ *                  layouts say rows of d elements, a page stands for its
+ *                  group's 16 rows: a full store is [B, Hkv, ceil(L/16)]
+ *                  pages, windows [B, Hkv, W * G], gathered buffers
+ *                  [B, Hkv, nQC, top_k_groups], pools [B, Hkv, n_slots].
+ *                  Written by hga_store_kv and read back by hga_load_kv.
+ *                  Needs dtype HGA_BF16 and head_dim 128; any seq_len. Read by
+ *                  every attention call, prefill (q_len > 1) among them, and
+ *                  moved by the gathers; a rotated-key output of the summary
+ *                  calls returns HGA_ERR_UNSUPPORTED. Rows at positions after
+ *                  a call's last query may hold anything; a row whose scale
+ *                  code is NaN makes NaN what attends to it, nothing else. */
+typedef enum { HGA_KV_AS_DTYPE = 0, HGA_KV_E4M3 = 1, HGA_KV_E2M1 = 2 } hga_kv_type;
+
+#define HGA_E2M1_PAGE 1152 /* bytes of 16 tokens' rows of one tensor, HGA_KV_E2M1 */
 
 /* Which heads route.
  * HGA_ROUTE_PER_KV_HEAD: one routing query per (sequence, KV head, query
@@ -169,6 +192,20 @@ typedef struct {
     int32_t routing;           /* hga_routing (0 = per KV head) */
 } hga_config;
 
+/* Rotary positions with several axes (time, height and width of a video's
+ * tokens, say). Every token has one position per axis; pair i turns by
+ * positions[pair_axis[i]] * theta_i, with theta_i as in the conventions above.
+ * A pair whose entry is -1 is not rotated but copied. Contiguous and
+ * interleaved sections are both lists of this kind. inverse = 1 turns by the
+ * negative angle: the inverse rotation, which is also the gradient of the
+ * rotation (its matrix is orthogonal). A host struct, read during the call. */
+typedef struct {
+    int32_t n_axes;            /* 1 .. HGA_MAX_AXES */
+    int32_t inverse;           /* 0 or 1 */
+    int8_t pair_axis[64];      /* entries i < d/2: -1 .. n_axes - 1 */
+} hga_rope_axes;
+#define HGA_MAX_AXES 4
+
 /* Rotate x by RoPE (standard rotary position embedding; the summaries of
  * "Kernmechanisme" item 3 are built on it). x, x_rot: [n_outer, n_tokens,
  * n_heads, d] of cfg->dtype; token t sits at position pos0 + t. x_rot may
@@ -177,6 +214,19 @@ typedef struct {
  * with pos0 = 0. */
 hga_status hga_apply_rope(const hga_config* cfg, const void* x, void* x_rot, int64_t n_outer,
                           int64_t n_tokens, int32_t n_heads, int64_t pos0, void* stream);
+
+/* hga_apply_rope with several position axes (no counterpart in the pages).
+ * x, x_rot: [n_outer, n_tokens, n_heads, d] of cfg->dtype; x_rot may equal x
+ * (in place). positions: int32 [n_axes, n_batch, n_tokens], any values; the
+ * n_outer rows are n_batch sequences of n_outer / n_batch rows each (which
+ * must divide), and the rows of a sequence share its positions. Uses
+ * cfg->head_dim, rope_theta and dtype only. Typical uses: queries
+ * [B, q_len, Hq, d] with n_outer = n_batch = B; keys [B*Hkv, L, 1, d] with
+ * n_outer = B*Hkv, n_batch = B; a gradient by axes->inverse = 1. */
+hga_status hga_apply_rope_axes(const hga_config* cfg, const hga_rope_axes* axes,
+                               const int32_t* positions, const void* x, void* x_rot,
+                               int64_t n_batch, int64_t n_outer, int64_t n_tokens,
+                               int32_t n_heads, void* stream);
 
 /* RoPE-aware chunk and group key summaries ("Kernmechanisme" item 3) of the
  * chunks [chunk_begin, chunk_end) from the pre-RoPE projected keys k_raw
@@ -193,6 +243,41 @@ hga_status hga_apply_rope(const hga_config* cfg, const void* x, void* x_rot, int
 hga_status hga_build_summaries(const hga_config* cfg, const void* k_raw, void* chunk_sum,
                                void* group_sum, void* k_rot_out, int32_t chunk_begin,
                                int32_t chunk_end, void* stream);
+
+/* hga_build_summaries for keys whose positions have several axes (no
+ * counterpart in the pages): R(p_t theta_i) uses the token's position on the
+ * pair's axis, and R(pbar theta_i) the mean of that axis' positions over the
+ * set; a pair on no axis (-1) is a plain mean. positions: int32
+ * [n_axes, B, L]. axes->inverse must be 0 (HGA_ERR_CONFIG). All else as
+ * hga_build_summaries; routing and attention then need no positions (they
+ * go by the order of the tokens). */
+hga_status hga_build_summaries_axes(const hga_config* cfg, const hga_rope_axes* axes,
+                                    const int32_t* positions, const void* k_raw, void* chunk_sum,
+                                    void* group_sum, void* k_rot_out, int32_t chunk_begin,
+                                    int32_t chunk_end, void* stream);
+
+/* Write the keys and values of tokens [pos0, pos0 + n_tokens) into a store of
+ * kv_type HGA_KV_E2M1 (no counterpart in the pages; other types are copied by
+ * the caller: HGA_ERR_UNSUPPORTED). k, v: [B, Hkv, n_tokens, d] bf16.
+ * k_store, v_store: [B, Hkv, ceil(L/16)] pages; only the given tokens' rows
+ * change. With axes == NULL (and positions == NULL) the keys are stored as
+ * given (already rotated); otherwise they are rotated first, in 64 bits and
+ * rounded to fp32, by positions [n_axes, B, n_tokens] int32, or, where positions is NULL (n_axes
+ * must be 1), by pos0 + t. axes->inverse must be 0.
+ * Rounding, in fp32: block scale = E4M3(amax / (6 * tensor scale)) (nearest
+ * even, at most 448), S = block scale * tensor scale, code = E2M1(x / S)
+ * (nearest even, at most 6); a block whose S is 0 is all zero; a block with a
+ * NaN or an infinity gets a NaN scale. A tensor scale that is a power of two
+ * near amax(tensor) / 2688 uses the range of the block scales and makes every
+ * stored value a bf16 number. */
+hga_status hga_store_kv(const hga_config* cfg, const hga_rope_axes* axes,
+                        const int32_t* positions, const void* k, const void* v, void* k_store,
+                        void* v_store, int64_t pos0, int64_t n_tokens, void* stream);
+
+/* Read tokens [pos0, pos0 + n_tokens) of such a store back: k, v
+ * [B, Hkv, n_tokens, d] bf16, each value rounded once (nearest even). */
+hga_status hga_load_kv(const hga_config* cfg, const void* k_store, const void* v_store, void* k,
+                       void* v, int64_t pos0, int64_t n_tokens, void* stream);
 
 /* Level-1 routing ("Kernmechanisme" item 2, Niveau 1, and Deterministische
  * Zichtbaarheid). For every (b, KV head, query chunk j of the span): q-bar

@@ -97,10 +97,11 @@ hga_status make_params(const hga_config* c, Params* p) {
     if (c->kv_layout != HGA_KV_FULL && c->kv_layout != HGA_KV_WINDOWS) return HGA_ERR_CONFIG;
     if (c->summary_type != HGA_SUMMARY_F32 && c->summary_type != HGA_SUMMARY_BF16)
         return HGA_ERR_CONFIG;
-    if (c->kv_type != HGA_KV_AS_DTYPE && c->kv_type != HGA_KV_E4M3) return HGA_ERR_CONFIG;
+    if (c->kv_type != HGA_KV_AS_DTYPE && c->kv_type != HGA_KV_E4M3 && c->kv_type != HGA_KV_E2M1)
+        return HGA_ERR_CONFIG;
     if (c->routing != HGA_ROUTE_PER_KV_HEAD && c->routing != HGA_ROUTE_PER_Q_HEAD)
         return HGA_ERR_CONFIG;
-    if (c->kv_type == HGA_KV_E4M3) {
+    if (c->kv_type != HGA_KV_AS_DTYPE) {
         if (!(c->k_scale > 0.0f) || !isfinite(c->k_scale) || !(c->v_scale > 0.0f) ||
             !isfinite(c->v_scale))
             return HGA_ERR_CONFIG;
@@ -136,9 +137,13 @@ hga_status make_params(const hga_config* c, Params* p) {
     p->kv_layout = c->kv_layout;
     p->sum_bf16 = c->summary_type == HGA_SUMMARY_BF16 ? 1 : 0;
     p->kv_f8 = c->kv_type == HGA_KV_E4M3 ? 1 : 0;
-    p->kv_es = p->kv_f8 ? 1 : (c->dtype == HGA_BF16 ? 2 : 4);
-    p->k_scale = p->kv_f8 ? c->k_scale : 1.0f;
-    p->v_scale = p->kv_f8 ? c->v_scale : 1.0f;
+    p->kv_f4 = c->kv_type == HGA_KV_E2M1 ? 1 : 0;
+    const int es = p->kv_f8 ? 1 : (c->dtype == HGA_BF16 ? 2 : 4);
+    p->kv_blk = p->kv_f4 ? kE2m1Page : kGroupRows * c->head_dim * es;
+    p->kv_slab = p->kv_f4 ? ((int64_t)c->seq_len + kGroupRows - 1) / kGroupRows * kE2m1Page
+                          : (int64_t)c->seq_len * c->head_dim * es;
+    p->k_scale = p->kv_f8 || p->kv_f4 ? c->k_scale : 1.0f;
+    p->v_scale = p->kv_f8 || p->kv_f4 ? c->v_scale : 1.0f;
     for (int i = 0; i < kMaxHalfDim; ++i)
         p->inv_freq[i] = i < c->head_dim / 2
                              ? pow(c->rope_theta, -2.0 * (double)i / (double)c->head_dim)
@@ -157,6 +162,23 @@ hga_status cuda_failed(cudaError_t e) {
 }
 
 hga_status launched(cudaError_t e) { return e == cudaSuccess ? HGA_OK : cuda_failed(e); }
+
+// Kernel-side axes. NULL: no rotation (n_axes 0).
+hga_status make_axes(const Params& p, const hga_rope_axes* a, bool may_invert, AxisMap* am) {
+    am->n_axes = 0;
+    am->sign = 1.0f;
+    for (int i = 0; i < kMaxHalfDim; ++i) am->axis[i] = -1;
+    if (a == nullptr) return HGA_OK;
+    if (a->n_axes < 1 || a->n_axes > HGA_MAX_AXES) return HGA_ERR_CONFIG;
+    if (a->inverse != 0 && !(may_invert && a->inverse == 1)) return HGA_ERR_CONFIG;
+    for (int i = 0; i < p.d / 2; ++i) {
+        if (a->pair_axis[i] < -1 || a->pair_axis[i] >= a->n_axes) return HGA_ERR_CONFIG;
+        am->axis[i] = a->pair_axis[i];
+    }
+    am->n_axes = a->n_axes;
+    am->sign = a->inverse ? -1.0f : 1.0f;
+    return HGA_OK;
+}
 
 // Last step before any launch: attach the current device's error word. (A
 // call's stream must belong to the current device; that is the caller's
@@ -197,6 +219,7 @@ cudaError_t set_func_attr_once(const void* fn, cudaFuncAttribute attr, int value
 
 using namespace hga;
 
+static_assert(sizeof(hga_rope_axes) == 72, "hga_rope_axes layout is part of the ABI");
 static_assert(sizeof(hga_config) == 96, "hga_config layout is part of the ABI");
 static_assert(offsetof(hga_config, routing) == 88, "hga_config layout is part of the ABI");
 static_assert(offsetof(hga_config, summary_type) == 72, "hga_config layout is part of the ABI");
@@ -206,7 +229,7 @@ static_assert(offsetof(hga_config, rope_theta) == 48, "hga_config layout is part
 
 extern "C" {
 
-int32_t hga_version(void) { return 10800; }
+int32_t hga_version(void) { return 10900; }
 
 int32_t hga_last_cuda_error(void) { return g_last_cuda_error; }
 
@@ -266,10 +289,101 @@ hga_status hga_build_summaries(const hga_config* cfg, const void* k_raw, void* c
     if (!aligned16(k_raw) || !aligned16(chunk_sum) || !aligned16(group_sum) ||
         (k_rot_out && !aligned16(k_rot_out)))
         return HGA_ERR_ALIGN;
-    if (k_rot_out && p.kv_f8) return HGA_ERR_UNSUPPORTED;  // rotated keys are written in dtype
+    if (k_rot_out && (p.kv_f8 || p.kv_f4))
+        return HGA_ERR_UNSUPPORTED;  // rotated keys are written in dtype
     HGA_ATTACH_ERR(p);
     return launched(launch_summaries(p, k_raw, chunk_sum, group_sum, k_rot_out, chunk_begin,
                                      chunk_end, (cudaStream_t)stream));
+}
+
+hga_status hga_apply_rope_axes(const hga_config* cfg, const hga_rope_axes* axes,
+                               const int32_t* positions, const void* x, void* x_rot,
+                               int64_t n_batch, int64_t n_outer, int64_t n_tokens,
+                               int32_t n_heads, void* stream) {
+    Params p;
+    AxisMap am;
+    hga_status s = make_params(cfg, &p);
+    if (s != HGA_OK) return s;
+    if (axes == nullptr) return HGA_ERR_NULL;
+    if ((s = make_axes(p, axes, true, &am)) != HGA_OK) return s;
+    if (n_batch < 0 || n_outer < 0 || n_tokens < 0 || n_heads < 1 || n_tokens > INT32_MAX ||
+        n_outer > INT32_MAX)
+        return HGA_ERR_SHAPE;
+    if (n_outer == 0 || n_tokens == 0) return HGA_OK;
+    if (n_batch < 1 || n_outer % n_batch) return HGA_ERR_SHAPE;
+    if (n_outer > INT64_MAX / 1024 / n_tokens / n_heads) return HGA_ERR_SHAPE;
+    if (positions == nullptr || x == nullptr || x_rot == nullptr) return HGA_ERR_NULL;
+    if (!aligned16(positions) || !aligned16(x) || !aligned16(x_rot)) return HGA_ERR_ALIGN;
+    HGA_ATTACH_ERR(p);
+    return launched(launch_rope_axes(p, am, positions, x, x_rot, n_batch, n_outer, n_tokens,
+                                     n_heads, (cudaStream_t)stream));
+}
+
+hga_status hga_build_summaries_axes(const hga_config* cfg, const hga_rope_axes* axes,
+                                    const int32_t* positions, const void* k_raw, void* chunk_sum,
+                                    void* group_sum, void* k_rot_out, int32_t chunk_begin,
+                                    int32_t chunk_end, void* stream) {
+    Params p;
+    AxisMap am;
+    hga_status s = make_params(cfg, &p);
+    if (s != HGA_OK) return s;
+    if (axes == nullptr) return HGA_ERR_NULL;
+    if ((s = make_axes(p, axes, false, &am)) != HGA_OK) return s;
+    if (chunk_begin < 0 || chunk_end < chunk_begin || chunk_end > p.nC) return HGA_ERR_SHAPE;
+    if (chunk_end == chunk_begin) return HGA_OK;
+    if (positions == nullptr || k_raw == nullptr || chunk_sum == nullptr || group_sum == nullptr)
+        return HGA_ERR_NULL;
+    if (!aligned16(positions) || !aligned16(k_raw) || !aligned16(chunk_sum) ||
+        !aligned16(group_sum) || (k_rot_out && !aligned16(k_rot_out)))
+        return HGA_ERR_ALIGN;
+    if (k_rot_out && (p.kv_f8 || p.kv_f4))
+        return HGA_ERR_UNSUPPORTED;  // rotated keys are written in dtype
+    HGA_ATTACH_ERR(p);
+    return launched(launch_summaries_axes(p, am, positions, k_raw, chunk_sum, group_sum, k_rot_out,
+                                          chunk_begin, chunk_end, (cudaStream_t)stream));
+}
+
+// Shared checks of hga_store_kv / hga_load_kv.
+static hga_status check_store_args(const Params& p, const void* k, const void* v,
+                                   const void* k_store, const void* v_store, int64_t pos0,
+                                   int64_t n_tokens) {
+    if (!p.kv_f4) return HGA_ERR_UNSUPPORTED;
+    if (pos0 < 0 || n_tokens < 0 || pos0 > p.L || n_tokens > p.L - pos0) return HGA_ERR_SHAPE;
+    if (n_tokens == 0) return HGA_OK;
+    if (!k || !v || !k_store || !v_store) return HGA_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_store) || !aligned16(v_store))
+        return HGA_ERR_ALIGN;
+    return HGA_OK;
+}
+
+hga_status hga_store_kv(const hga_config* cfg, const hga_rope_axes* axes,
+                        const int32_t* positions, const void* k, const void* v, void* k_store,
+                        void* v_store, int64_t pos0, int64_t n_tokens, void* stream) {
+    Params p;
+    AxisMap am;
+    hga_status s = make_params(cfg, &p);
+    if (s != HGA_OK) return s;
+    if ((s = make_axes(p, axes, false, &am)) != HGA_OK) return s;
+    s = check_store_args(p, k, v, k_store, v_store, pos0, n_tokens);
+    if (s != HGA_OK || n_tokens == 0) return s;
+    if (axes == nullptr && positions != nullptr) return HGA_ERR_CONFIG;
+    if (axes != nullptr && positions == nullptr && axes->n_axes != 1) return HGA_ERR_NULL;
+    if (positions && !aligned16(positions)) return HGA_ERR_ALIGN;
+    HGA_ATTACH_ERR(p);
+    return launched(launch_store_kv(p, am, positions, k, v, k_store, v_store, pos0, n_tokens,
+                                    (cudaStream_t)stream));
+}
+
+hga_status hga_load_kv(const hga_config* cfg, const void* k_store, const void* v_store, void* k,
+                       void* v, int64_t pos0, int64_t n_tokens, void* stream) {
+    Params p;
+    hga_status s = make_params(cfg, &p);
+    if (s != HGA_OK) return s;
+    s = check_store_args(p, k, v, k_store, v_store, pos0, n_tokens);
+    if (s != HGA_OK || n_tokens == 0) return s;
+    HGA_ATTACH_ERR(p);
+    return launched(launch_load_kv(p, k_store, v_store, k, v, pos0, n_tokens,
+                                   (cudaStream_t)stream));
 }
 
 hga_status hga_route_chunks(const hga_config* cfg, const void* q_rot, const void* chunk_sum,

@@ -17,6 +17,8 @@ namespace hga {
 constexpr int kMaxHalfDim = 64;      // head_dim <= 128
 constexpr int kGroupRows = 16;       // g = C / G: one group = 16 token rows
 constexpr int kMaxForced = 64;       // n_sink + n_local + 1 chunks at most
+constexpr int kE2m1Page = HGA_E2M1_PAGE;            // bytes of 16 E2M1 rows: codes, then scales
+constexpr int kE2m1Codes = kGroupRows * 64;         // bytes of a page's codes: 4 tiles of 16 x 16
 
 // Kernel-side copy of the configuration, passed by value.
 struct Params {
@@ -28,9 +30,11 @@ struct Params {
     int Hu;                        // routing units per sequence: Hkv, or Hq (per query head);
                                    // gq = query heads per unit; unit h reads KV head
                                    // h / (Hu / Hkv)
-    int kv_f8;                     // K/V stored as E4M3 codes (else dtype)
-    int kv_es;                     // bytes per K/V element
-    float k_scale, v_scale;        // E4M3 code scales (1 otherwise)
+    int kv_f8;                     // K/V stored as E4M3 codes (else dtype, or E2M1)
+    int kv_f4;                     // K/V stored as pages of E2M1 codes
+    int kv_blk;                    // bytes of a 16-row K (or V) block
+    int64_t kv_slab;               // bytes of one (sequence, KV head) of a full K (or V) store
+    float k_scale, v_scale;        // E4M3 / E2M1 tensor scales (1 otherwise)
     int* err;                      // device error word, never NULL
     unsigned long long wait_ns;    // limit of each bounded device wait
     double inv_freq[kMaxHalfDim];  // rope_theta^(-2i/d), computed on the host in double
@@ -69,6 +73,13 @@ __host__ __device__ __forceinline__ int forced_chunks(const Params& p, int j, in
 __host__ __device__ __forceinline__ bool is_forced(const Params& p, int j, int c) {
     return c == j || (c >= 0 && c < p.n_sink && c <= j) || (c < j && c >= j - p.n_local);
 }
+
+// Kernel-side hga_rope_axes.
+struct AxisMap {
+    int n_axes;
+    float sign;                    // +1, or -1: the inverse rotation
+    int8_t axis[kMaxHalfDim];      // of pair i, -1: not rotated
+};
 
 // cos / sin of position * inv_freq. The product is formed and reduced to
 // [-pi, pi] in double (Cody-Waite style reduction by 2*pi); the fast

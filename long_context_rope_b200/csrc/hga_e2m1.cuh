@@ -1,0 +1,101 @@
+// hga_e2m1.cuh -- the 4-bit key/value store: pages, codes and block scales.
+//
+// A page holds the rows of 16 tokens of one tensor (d = 128): the codes as
+// four tiles of 32 dims, each 16 rows x 16 bytes, then 16 rows x 8 E4M3
+// scales (one per 16 dims). Tiles, not whole rows: eight rows' 16-byte pieces
+// of a tile are 128 contiguous bytes, so the 8x8 matrix loads of decode
+// attention (ldmatrix) touch every shared-memory bank once.
+#pragma once
+
+#include "hga_common.cuh"
+
+namespace hga {
+namespace e2m1 {
+
+constexpr int kBlock = 16;           // dims that share a scale
+constexpr int kScales = 128 / kBlock;
+
+// Byte offsets in a page.
+__host__ __device__ constexpr int code_at(int row, int dim) {
+    return (dim >> 5) * (kGroupRows * 16) + row * 16 + ((dim & 31) >> 1);
+}
+__host__ __device__ constexpr int scale_at(int row, int block) {
+    return kE2m1Codes + row * kScales + block;
+}
+
+// Eight codes (bits 4i..4i+3 of w) to four f16 pairs; exact, as every E2M1
+// number is an f16 number.
+__device__ __forceinline__ void codes_to_f16x2(uint32_t w, uint32_t (&f)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+        : "r"(w));
+}
+
+// Eight floats to codes, nearest even, at most 6 in magnitude.
+__device__ __forceinline__ uint32_t f32x8_to_codes(const float* q) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    return w;
+}
+
+// The E4M3 code of x >= 0, nearest even, at most 448.
+__device__ __forceinline__ uint32_t scale_code(float x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+    return r & 0xffu;
+}
+
+// Two E4M3 codes (low and high byte) to an f16 pair, exact.
+__device__ __forceinline__ uint32_t scales_to_f16x2(uint16_t x) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+    return r;
+}
+
+__device__ __forceinline__ float scale_value(uint32_t code) {
+    const uint32_t h = scales_to_f16x2((uint16_t)code);
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                              *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Sixteen elements of one block: their codes and the block's scale code, by
+// the rounding that hga_store_kv states. `ts` is the tensor scale. The divide
+// is the correctly rounded one: of bf16 elements and a power-of-two ts the
+// quotients that lie halfway between two codes are met exactly.
+__device__ __forceinline__ void quantise16(const float (&x)[kBlock], float ts, uint2& codes,
+                                           uint32_t& scale) {
+    float amax = 0.f;  // NaN if any element is
+#pragma unroll
+    for (int e = 0; e < kBlock; ++e)
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(x[e])));
+    codes = make_uint2(0u, 0u);
+    if (!(amax < INFINITY)) {
+        scale = 0x7fu;  // NaN: the block's values are NaN
+        return;
+    }
+    scale = scale_code(amax / (6.f * ts));
+    const float S = scale_value(scale) * ts;
+    if (!(S > 0.f)) {
+        scale = 0u;
+        return;
+    }
+    float q[kBlock];
+#pragma unroll
+    for (int e = 0; e < kBlock; ++e) q[e] = x[e] / S;
+    codes = make_uint2(f32x8_to_codes(q), f32x8_to_codes(q + 8));
+}
+
+}  // namespace e2m1
+}  // namespace hga

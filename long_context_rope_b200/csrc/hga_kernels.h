@@ -32,6 +32,22 @@ cudaError_t launch_summaries(const Params& p, const void* k_raw, void* chunk_sum
                              void* group_sum, void* k_rot, int chunk_begin, int chunk_end,
                              cudaStream_t st);
 
+// Rotation by positions with several axes; n_outer is a multiple of n_batch.
+cudaError_t launch_rope_axes(const Params& p, const AxisMap& am, const int32_t* positions,
+                             const void* x, void* y, int64_t n_batch, int64_t n_outer,
+                             int64_t n_tokens, int n_heads, cudaStream_t st);
+cudaError_t launch_summaries_axes(const Params& p, const AxisMap& am, const int32_t* positions,
+                                  const void* k_raw, void* chunk_sum, void* group_sum,
+                                  void* k_rot, int chunk_begin, int chunk_end, cudaStream_t st);
+
+// The E2M1 store: rows [pos0, pos0 + n_tokens) of every (sequence, KV head).
+// am.n_axes == 0: keys stored as given.
+cudaError_t launch_store_kv(const Params& p, const AxisMap& am, const int32_t* positions,
+                            const void* k, const void* v, void* k_store, void* v_store,
+                            int64_t pos0, int64_t n_tokens, cudaStream_t st);
+cudaError_t launch_load_kv(const Params& p, const void* k_store, const void* v_store, void* k,
+                           void* v, int64_t pos0, int64_t n_tokens, cudaStream_t st);
+
 cudaError_t launch_qbar(const Params& p, const void* q_rot, float* qbar, cudaStream_t st);
 
 // Level-1 routing. q-bar must already be in `qbar` unless

@@ -275,7 +275,7 @@ cudaError_t launch_attend_decode(const Params& p, const void* q_rot, const KvSou
 }
 
 bool decode_kernel_supports(const Params& p) {
-    return p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.gq <= 8 &&
+    return !p.kv_f4 && p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.gq <= 8 &&
            p.L % kGroupRows == 0;
 }
 

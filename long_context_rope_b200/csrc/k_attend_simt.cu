@@ -11,8 +11,11 @@
 // (sequence, KV head, query chunk) unit; 4 warps x 4 rows. Keys stream
 // through shared memory 32 at a time (two 16-row blocks) as fp32; lane i of
 // a warp scores key i, then the online-softmax state of the row is updated
-// and each lane accumulates d/32 output columns.
+// and each lane accumulates d/32 output columns. E2M1 keys and values (kF4,
+// d = 128) are read from their pages and widened to fp32 as they are staged;
+// the tensor scales multiply the scores and the normalised output.
 #include "hga_blocks.cuh"
+#include "hga_e2m1.cuh"
 #include "hga_kernels.h"
 
 namespace hga {
@@ -37,7 +40,7 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-template <typename T, int D>
+template <typename T, int D, bool kF4>
 __global__ void __launch_bounds__(128) attend_simt_kernel(Params p, const T* __restrict__ q,
                                                           KvSources kv,
                                                           const int32_t* __restrict__ sel,
@@ -90,11 +93,32 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(Params p, const T* __r
     const int64_t res_slab = (int64_t)(p.kv_layout == HGA_KV_WINDOWS
                                            ? (int64_t)(p.n_sink + p.n_local + 1) * p.C
                                            : p.L);
-    const T* kres = (const T*)kv.k_res + bh * res_slab * D;
-    const T* vres = (const T*)kv.v_res + bh * res_slab * D;
-    const T* kgat = gathered ? (const T*)kv.k_gat + prob * (int64_t)p.kg * kGroupRows * D : nullptr;
-    const T* vgat = gathered ? (const T*)kv.v_gat + prob * (int64_t)p.kg * kGroupRows * D : nullptr;
-    const float scale = 1.4426950408889634f / sqrtf((float)D);
+    // bytes of one unit's share of the resident and of the gathered buffers
+    const int64_t res_bytes = (res_slab + kGroupRows - 1) / kGroupRows * kE2m1Page;
+    const int64_t gat_rows = (int64_t)p.kg * kGroupRows;
+    auto unit = [&](const void* base, int64_t of, int64_t rows, int64_t bytes) -> const T* {
+        if constexpr (kF4) return (const T*)((const uint8_t*)base + of * bytes);
+        return (const T*)base + of * rows * D;
+    };
+    const T* kres = unit(kv.k_res, bh, res_slab, res_bytes);
+    const T* vres = unit(kv.v_res, bh, res_slab, res_bytes);
+    const T* kgat = gathered ? unit(kv.k_gat, prob, gat_rows, (int64_t)p.kg * kE2m1Page) : nullptr;
+    const T* vgat = gathered ? unit(kv.v_gat, prob, gat_rows, (int64_t)p.kg * kE2m1Page) : nullptr;
+    const float scale = 1.4426950408889634f / sqrtf((float)D) * p.k_scale;
+    // element e of row `row` of a unit's keys or values
+    auto element = [&](const T* base, int64_t row, int e) -> float {
+        if constexpr (kF4) {
+            const uint8_t* pg = (const uint8_t*)base + row / kGroupRows * kE2m1Page;
+            const int r = (int)(row % kGroupRows);
+            const uint32_t byte = pg[e2m1::code_at(r, e)];
+            uint32_t f[4];
+            e2m1::codes_to_f16x2((e & 1) ? byte >> 4 : byte, f);
+            const float v = __half2float(__ushort_as_half((unsigned short)(f[0] & 0xffffu)));
+            return v * e2m1::scale_value(pg[e2m1::scale_at(r, e / e2m1::kBlock)]);
+        } else {
+            return to_f(base[row * D + e]);
+        }
+    };
 
     float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][NE];
     int qpos[kRowsPerWarp];
@@ -118,17 +142,12 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(Params p, const T* __r
             if (bi < nb) {
                 const int rw = blk_row[bi];
                 const int pos = blk_pos[bi] + kr % kGroupRows;
-                if (pos < p.L) {
-                    int64_t off;
-                    if (rw & kSrcGathered) {
-                        off = (int64_t)((rw & ~kSrcGathered) + kr % kGroupRows) * D + e;
-                        kvk = to_f(kgat[off]);
-                        kvv = to_f(vgat[off]);
-                    } else {
-                        off = (int64_t)(rw + kr % kGroupRows) * D + e;
-                        kvk = to_f(kres[off]);
-                        kvv = to_f(vres[off]);
-                    }
+                // E2M1: rows after the span's last query may hold anything
+                if (pos < (kF4 ? (int)span_end : p.L)) {
+                    const bool gat = (rw & kSrcGathered) != 0;
+                    const int64_t row = (rw & ~kSrcGathered) + kr % kGroupRows;
+                    kvk = element(gat ? kgat : kres, row, e);
+                    kvv = element(gat ? vgat : vres, row, e);
                 }
             }
             sk[kr][e] = kvk;
@@ -157,7 +176,7 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(Params p, const T* __r
             const float mn = fmaxf(m[i], mt);
             float pr, alpha;
             if (mn == -INFINITY) {
-                pr = 0.f;
+                pr = kF4 && isnan(s) ? s : 0.f;  // a NaN score makes its rows NaN
                 alpha = 1.f;
             } else {
                 pr = vis ? exp2f(s - mn) : 0.f;
@@ -171,7 +190,13 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(Params p, const T* __r
             for (int kk = 0; kk < kTileKeys; ++kk) {
                 const float pk = __shfl_sync(0xffffffffu, pr, kk);
 #pragma unroll
-                for (int e = 0; e < NE; ++e) acc[i][e] = fmaf(pk, sv[kk][lane + 32 * e], acc[i][e]);
+                for (int e = 0; e < NE; ++e) {
+                    float vv = sv[kk][lane + 32 * e];
+                    // a NaN in a value of the chunk that this query does not see
+                    if (kF4 && blk_pos[min(b0 + kk / kGroupRows, nb - 1)] + kk % kGroupRows > qpos[i])
+                        vv = 0.f;
+                    acc[i][e] = fmaf(pk, vv, acc[i][e]);
+                }
             }
         }
     }
@@ -181,7 +206,8 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(Params p, const T* __r
         const int r = row0 + warp * kRowsPerWarp + i;
         const int t = pos_lo + r / p.gq - p.q_begin;
         const int hq = h * p.gq + r % p.gq;
-        const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
+        float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
+        if constexpr (kF4) inv = (isnan(l[i]) ? l[i] : inv) * p.v_scale;
         T* orow = out + (((int64_t)b * p.q_len + t) * p.Hq + hq) * D;
 #pragma unroll
         for (int e = 0; e < NE; ++e) orow[lane + 32 * e] = from_f<T>(acc[i][e] * inv);
@@ -196,20 +222,23 @@ cudaError_t launch_attend_simt(const Params& p, const void* q_rot, const KvSourc
     if (p.nQC == 0) return cudaSuccess;
     const int max_rows = (p.q_len < p.C ? p.q_len : p.C) * p.gq;
     dim3 grid((max_rows + kRowsPerCta - 1) / kRowsPerCta, p.nQC, p.B * p.Hkv);
-    if (p.dtype == HGA_BF16) {
+    if (p.kv_f4) {
+        attend_simt_kernel<__nv_bfloat16, 128, true><<<grid, 128, 0, st>>>(
+            p, (const __nv_bfloat16*)q_rot, kv, sel_groups, n_sel_groups, (__nv_bfloat16*)out);
+    } else if (p.dtype == HGA_BF16) {
         if (p.d == 128)
-            attend_simt_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(
+            attend_simt_kernel<__nv_bfloat16, 128, false><<<grid, 128, 0, st>>>(
                 p, (const __nv_bfloat16*)q_rot, kv, sel_groups, n_sel_groups, (__nv_bfloat16*)out);
         else
-            attend_simt_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(
+            attend_simt_kernel<__nv_bfloat16, 64, false><<<grid, 128, 0, st>>>(
                 p, (const __nv_bfloat16*)q_rot, kv, sel_groups, n_sel_groups, (__nv_bfloat16*)out);
     } else {
         if (p.d == 128)
-            attend_simt_kernel<float, 128><<<grid, 128, 0, st>>>(p, (const float*)q_rot, kv,
+            attend_simt_kernel<float, 128, false><<<grid, 128, 0, st>>>(p, (const float*)q_rot, kv,
                                                                  sel_groups, n_sel_groups,
                                                                  (float*)out);
         else
-            attend_simt_kernel<float, 64><<<grid, 128, 0, st>>>(p, (const float*)q_rot, kv,
+            attend_simt_kernel<float, 64, false><<<grid, 128, 0, st>>>(p, (const float*)q_rot, kv,
                                                                 sel_groups, n_sel_groups,
                                                                 (float*)out);
     }

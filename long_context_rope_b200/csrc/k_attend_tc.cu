@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 }  // namespace
 
 bool tc_kernel_supports(const Params& p, bool gathered) {
-    return p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.q_len > 1 && !gathered &&
+    return !p.kv_f4 && p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.q_len > 1 && !gathered &&
            p.kv_layout == HGA_KV_FULL && p.C % 32 == 0;
 }
 

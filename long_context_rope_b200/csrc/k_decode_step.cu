@@ -570,7 +570,7 @@ int step_cluster(const Params& p, size_t smem) {
 }  // namespace
 
 bool decode_step_supports(const Params& p) {
-    if (!(p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.gq <= 8 && p.L % kGroupRows == 0 &&
+    if (!(!p.kv_f4 && p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.gq <= 8 && p.L % kGroupRows == 0 &&
           p.kc <= kMaxKc && p.kg <= kMaxKg && p.nQC == 1))
         return false;
     for (int cl = 1; cl <= kMaxCluster; ++cl)

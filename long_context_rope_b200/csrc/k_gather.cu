@@ -6,7 +6,7 @@
 // (cold tier: the full K/V history in host RAM).
 //
 // HBM source: each 16-row group of K and of V is one contiguous block
-// (16 * d elements); per CTA one thread streams its groups through a ring of
+// (16 * d elements, or a page of E2M1 codes); per CTA one thread streams its groups through a ring of
 // shared-memory stages with bulk (TMA) loads and bulk stores.
 // Host source: the pinned host store is read with 16-byte loads through its
 // device mapping (zero-copy over the host link); every thread keeps several
@@ -51,8 +51,7 @@ __global__ void __launch_bounds__(32) gather_hbm_kernel(Params p, const char* __
     __shared__ __align__(8) uint64_t full[kGatherStages];
     __shared__ int64_t src_off[kGatherUnitsMax], dst_off[kGatherUnitsMax];
     const int lane = threadIdx.x;
-    const int es = p.kv_es;
-    const uint32_t blk = (uint32_t)(kGroupRows * p.d * es);
+    const uint32_t blk = (uint32_t)p.kv_blk;
     const int64_t total = (int64_t)p.B * p.Hkv * p.nQC * p.kg;
     const int64_t u0 = (int64_t)blockIdx.x * per;
     // validate this CTA's units; compact the valid ones, in unit order
@@ -78,7 +77,7 @@ __global__ void __launch_bounds__(32) gather_hbm_kernel(Params p, const char* __
                 const int c = gi >= 0 ? gi / p.G : -1;
                 if (gi >= 0 && c < j && !is_forced(p, j, c) && (s == 0 || gi > prev)) {
                     ok = true;
-                    so = bh * (int64_t)p.L * p.d * es + (int64_t)gi * blk;
+                    so = bh * p.kv_slab + (int64_t)gi * blk;
                     dof = u * (int64_t)blk;
                 } else {
                     raise_dev_error(p, kDevErrGroupIndex);
@@ -152,8 +151,7 @@ __global__ void __launch_bounds__(256) gather_host_kernel(Params p, const uint4*
     const int64_t bh = blockIdx.z;
     const int j = p.j0 + jj;
     const int64_t prob = bh * p.nQC + jj;
-    const int es = p.kv_es;
-    const int vec_per_blk = kGroupRows * p.d * es / 16;
+    const int vec_per_blk = p.kv_blk / 16;
     const int s_lo = blockIdx.x * kHostSlots;
     if (threadIdx.x < kHostSlots) {
         const int n = checked_count(p, nsel, prob);
@@ -161,7 +159,7 @@ __global__ void __launch_bounds__(256) gather_host_kernel(Params p, const uint4*
         s_gi[threadIdx.x] = s < n ? checked_group_entry(p, j, sel + prob * p.kg, s) : -1;
     }
     __syncthreads();
-    const int64_t src_base = bh * (int64_t)p.L * p.d * es / 16;
+    const int64_t src_base = bh * (p.kv_slab / 16);
     const int64_t dst_base = prob * (int64_t)p.kg * vec_per_blk;
     for (int v0 = threadIdx.x; v0 < vec_per_blk; v0 += blockDim.x) {
         uint4 kk[kHostSlots], vv[kHostSlots];
@@ -302,8 +300,7 @@ __global__ void __launch_bounds__(256) warm_copy_kernel(Params p, const uint4* _
     __shared__ int s_src[kHostSlots], s_gi[kHostSlots];
     const int64_t bh = blockIdx.z;
     const int64_t prob = bh * p.nQC;
-    const int es = p.kv_es;
-    const int vec_per_blk = kGroupRows * p.d * es / 16;
+    const int vec_per_blk = p.kv_blk / 16;
     const int s_lo = blockIdx.x * kHostSlots;
     if (threadIdx.x < kHostSlots) {
         const int s = s_lo + threadIdx.x;
@@ -311,7 +308,7 @@ __global__ void __launch_bounds__(256) warm_copy_kernel(Params p, const uint4* _
         s_gi[threadIdx.x] = s < p.kg ? sel[prob * p.kg + s] : -1;
     }
     __syncthreads();
-    const int64_t host_base = bh * (int64_t)p.L * p.d * es / 16;
+    const int64_t host_base = bh * (p.kv_slab / 16);
     const int64_t pool_base = bh * (int64_t)n_slots * vec_per_blk;
     const int64_t dst_base = prob * (int64_t)p.kg * vec_per_blk;
     for (int v0 = threadIdx.x; v0 < vec_per_blk; v0 += blockDim.x) {
@@ -378,14 +375,13 @@ cudaError_t launch_gather(const Params& p, const void* k_src, const void* v_src,
                           const int32_t* sel_groups, const int32_t* n_sel_groups, void* k_dst,
                           void* v_dst, cudaStream_t st) {
     if (p.nQC == 0) return cudaSuccess;
-    const int es = p.kv_es;
     if (from_host) {
         dim3 grid((p.kg + kHostSlots - 1) / kHostSlots, p.nQC, p.B * p.Hkv);
         gather_host_kernel<<<grid, 256, 0, st>>>(p, (const uint4*)k_src, (const uint4*)v_src,
                                                  sel_groups, n_sel_groups, (uint4*)k_dst,
                                                  (uint4*)v_dst);
     } else {
-        const size_t smem = (size_t)kGatherStages * 2 * kGroupRows * p.d * es;
+        const size_t smem = (size_t)kGatherStages * 2 * p.kv_blk;
         cudaError_t e = set_func_attr_once((const void*)gather_hbm_kernel,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kGatherStages * 2 * kGroupRows * 128 * 4);

@@ -23,7 +23,8 @@ HGA_OK = 0
 HGA_BF16, HGA_F32 = 0, 1
 HGA_KV_FULL, HGA_KV_WINDOWS = 0, 1
 HGA_SUMMARY_F32, HGA_SUMMARY_BF16 = 0, 1
-HGA_KV_AS_DTYPE, HGA_KV_E4M3 = 0, 1
+HGA_KV_AS_DTYPE, HGA_KV_E4M3, HGA_KV_E2M1 = 0, 1, 2
+HGA_E2M1_PAGE, HGA_MAX_AXES = 1152, 4
 HGA_ROUTE_PER_KV_HEAD, HGA_ROUTE_PER_Q_HEAD = 0, 1
 STATUS = {0: "HGA_OK", -1: "HGA_ERR_NULL", -2: "HGA_ERR_SHAPE", -3: "HGA_ERR_ALIGN",
           -4: "HGA_ERR_CONFIG", -5: "HGA_ERR_CUDA", -6: "HGA_ERR_DEVICE_INDEX",
@@ -77,8 +78,17 @@ class HgaConfig(ctypes.Structure):
         return torch.bfloat16 if self.summary_type == HGA_SUMMARY_BF16 else torch.float32
 
     def kv_torch_dtype(self) -> torch.dtype:
-        """Element type of the key/value stores and buffers."""
+        """Element type of the key/value stores and buffers (E2M1: bytes of pages)."""
+        if self.kv_type == HGA_KV_E2M1:
+            return torch.uint8
         return torch.float8_e4m3fn if self.kv_type == HGA_KV_E4M3 else self.torch_dtype()
+
+    def kv_rows(self, *lead: int, rows: int) -> tuple:
+        """Shape of `rows` key or value rows per leading index: [*lead, rows, d],
+        or the pages that hold them, [*lead, ceil(rows / 16), 1152] (E2M1)."""
+        if self.kv_type == HGA_KV_E2M1:
+            return (*lead, -(-rows // 16), HGA_E2M1_PAGE)
+        return (*lead, rows, self.head_dim)
 
     def copy(self, **kw) -> "HgaConfig":
         c = HgaConfig()
@@ -86,6 +96,37 @@ class HgaConfig(ctypes.Structure):
         for k, v in kw.items():
             setattr(c, k, v)
         return c
+
+
+class HgaRopeAxes(ctypes.Structure):
+    """Mirror of hga_rope_axes (see rope_axes)."""
+    _fields_ = [("n_axes", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("pair_axis", ctypes.c_int8 * 64)]
+
+
+def pair_axes(half: int, sections, interleaved: bool = False) -> list:
+    """The axis of each of `half` rotary pairs: sections[a] pairs on axis a, one
+    section after another, or taken in turn while they last (interleaved);
+    -1 (not rotated) for pairs past the sections."""
+    left = [int(n) for n in sections]
+    if min(left, default=0) < 0 or sum(left) > half:
+        raise ValueError(f"sections {left} must be non-negative and sum to at most {half}")
+    if not interleaved:
+        out = [a for a, n in enumerate(left) for _ in range(n)]
+    else:
+        out = [a for i in range(max(left, default=0)) for a, n in enumerate(left) if i < n]
+    return out + [-1] * (half - len(out))
+
+
+def rope_axes(pair_axis, n_axes: int, inverse: bool = False) -> HgaRopeAxes:
+    """hga_rope_axes from the axis of each pair (pair_axes makes such lists)."""
+    pair_axis = [int(a) for a in pair_axis]
+    if len(pair_axis) > 64 or any(not -128 <= a < 128 for a in pair_axis):
+        raise ValueError("pair_axis: at most 64 entries of -1 .. n_axes - 1")
+    s = HgaRopeAxes(n_axes=int(n_axes), inverse=int(bool(inverse)))
+    for i in range(64):
+        s.pair_axis[i] = pair_axis[i] if i < len(pair_axis) else -1
+    return s
 
 
 def _load():
@@ -96,7 +137,12 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     C = ctypes.POINTER(HgaConfig)
+    A = ctypes.POINTER(HgaRopeAxes)
     sig = {
+        "hga_apply_rope_axes": [C, A, P, P, P, I64, I64, I64, I32, P],
+        "hga_build_summaries_axes": [C, A, P, P, P, P, P, I32, I32, P],
+        "hga_store_kv": [C, A, P, P, P, P, P, I64, I64, P],
+        "hga_load_kv": [C, P, P, P, P, I64, I64, P],
         "hga_apply_rope": [C, P, P, I64, I64, I32, I64, P],
         "hga_build_summaries": [C, P, P, P, P, I32, I32, P],
         "hga_route_chunks": [C, P, P, P, P, P, P, P],
@@ -196,6 +242,73 @@ def apply_rope(cfg: HgaConfig, x: torch.Tensor, x_rot: torch.Tensor, n_outer: in
                                n_tokens, n_heads, pos0, _stream(stream)), "hga_apply_rope")
 
 
+def apply_rope_axes(cfg: HgaConfig, axes: HgaRopeAxes, positions: torch.Tensor, x: torch.Tensor,
+                    x_rot: torch.Tensor, n_outer: int, n_tokens: int, n_heads: int,
+                    stream=None) -> None:
+    """Rotate by positions [n_axes, n_batch, n_tokens] int32 (see hga_apply_rope_axes)."""
+    shape = (n_outer, n_tokens, n_heads, cfg.head_dim)
+    if x.numel() != n_outer * n_tokens * n_heads * cfg.head_dim:
+        raise ValueError(f"x must hold {shape} elements")
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 3:
+        raise ValueError("positions must be a [n_axes, n_batch, n_tokens] tensor")
+    n_batch = int(positions.shape[1])
+    _check(_lib.hga_apply_rope_axes(
+        ctypes.byref(cfg), ctypes.byref(axes),
+        _ptr(positions, "positions", torch.int32, (axes.n_axes, n_batch, n_tokens)),
+        _ptr(x, "x", cfg.torch_dtype()), _ptr(x_rot, "x_rot", cfg.torch_dtype(), x.shape),
+        n_batch, n_outer, n_tokens, n_heads, _stream(stream)), "hga_apply_rope_axes")
+
+
+def build_summaries_axes(cfg: HgaConfig, axes: HgaRopeAxes, positions, k_raw, chunk_sum, group_sum,
+                         k_rot=None, chunk_begin=0, chunk_end=None, stream=None) -> None:
+    """build_summaries for keys at positions [n_axes, B, L] int32."""
+    B, H, L, d, nC, G = (cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_chunks,
+                         cfg.groups_per_chunk)
+    dt = cfg.torch_dtype()
+    _check(_lib.hga_build_summaries_axes(
+        ctypes.byref(cfg), ctypes.byref(axes),
+        _ptr(positions, "positions", torch.int32, (axes.n_axes, B, L)),
+        _ptr(k_raw, "k_raw", dt, (B, H, L, d)),
+        _ptr(chunk_sum, "chunk_sum", cfg.summary_torch_dtype(), (B, H, nC, d)),
+        _ptr(group_sum, "group_sum", cfg.summary_torch_dtype(), (B, H, nC * G, d)),
+        _ptr(k_rot, "k_rot", dt, (B, H, L, d), nullable=True), int(chunk_begin),
+        int(nC if chunk_end is None else chunk_end), _stream(stream)), "hga_build_summaries_axes")
+
+
+def store_kv(cfg: HgaConfig, k, v, k_store, v_store, pos0: int, axes: Optional[HgaRopeAxes] = None,
+             positions=None, stream=None) -> None:
+    """Quantise k, v [B, Hkv, n, d] into rows [pos0, pos0 + n) of an E2M1 store;
+    with axes the keys are rotated first (see hga_store_kv)."""
+    B, H, d = cfg.batch, cfg.n_kv_heads, cfg.head_dim
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, Hkv, n, d] tensor")
+    n = int(k.shape[2])
+    dt, store = torch.bfloat16, cfg.kv_rows(B, H, rows=cfg.seq_len)
+    if positions is not None and axes is None:
+        raise ValueError("positions need axes")
+    _check(_lib.hga_store_kv(
+        ctypes.byref(cfg), ctypes.byref(axes) if axes is not None else None,
+        _ptr(positions, "positions", torch.int32,
+             (axes.n_axes, B, n) if axes is not None else None, nullable=True),
+        _ptr(k, "k", dt, (B, H, n, d)), _ptr(v, "v", dt, (B, H, n, d)),
+        _ptr(k_store, "k_store", cfg.kv_torch_dtype(), store),
+        _ptr(v_store, "v_store", cfg.kv_torch_dtype(), store), int(pos0), n, _stream(stream)),
+        "hga_store_kv")
+
+
+def load_kv(cfg: HgaConfig, k_store, v_store, k, v, pos0: int, stream=None) -> None:
+    """Rows [pos0, pos0 + n) of an E2M1 store as bf16 k, v [B, Hkv, n, d]."""
+    B, H, d = cfg.batch, cfg.n_kv_heads, cfg.head_dim
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, Hkv, n, d] tensor")
+    n = int(k.shape[2])
+    dt, store = torch.bfloat16, cfg.kv_rows(B, H, rows=cfg.seq_len)
+    _check(_lib.hga_load_kv(
+        ctypes.byref(cfg), _ptr(k_store, "k_store", cfg.kv_torch_dtype(), store),
+        _ptr(v_store, "v_store", cfg.kv_torch_dtype(), store), _ptr(k, "k", dt, (B, H, n, d)),
+        _ptr(v, "v", dt, (B, H, n, d)), int(pos0), n, _stream(stream)), "hga_load_kv")
+
+
 def build_summaries(cfg: HgaConfig, k_raw, chunk_sum, group_sum, k_rot=None, chunk_begin=0,
                     chunk_end=None, stream=None) -> None:
     B, H, L, d, nC, G = (cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_chunks,
@@ -267,12 +380,12 @@ def decode_step(cfg: HgaConfig, q_rot, chunk_sum, group_sum, k_cache, v_cache, q
                 n_sel_chunks, sel_groups, n_sel_groups, out, stream=None) -> None:
     """Routing plus attention over the full resident cache (one launch for decode)."""
     B, H, L, d = cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim
-    dt, kvt = cfg.torch_dtype(), cfg.kv_torch_dtype()
+    dt, kvt, store = cfg.torch_dtype(), cfg.kv_torch_dtype(), cfg.kv_rows(B, H, rows=L)
     r = _route_ptrs(cfg, q_rot, chunk_sum, group_sum, qbar, sel_chunks, n_sel_chunks, sel_groups,
                     n_sel_groups)
     _check(_lib.hga_decode_step(
         ctypes.byref(cfg), r[0], r[1], r[2],
-        _ptr(k_cache, "k_cache", kvt, (B, H, L, d)), _ptr(v_cache, "v_cache", kvt, (B, H, L, d)),
+        _ptr(k_cache, "k_cache", kvt, store), _ptr(v_cache, "v_cache", kvt, store),
         *r[3:], _ptr(out, "out", dt, (B, cfg.q_len, cfg.n_q_heads, d)), _stream(stream)),
         "hga_decode_step")
 
@@ -284,13 +397,14 @@ def decode_step_tiered(cfg: HgaConfig, q_rot, chunk_sum, group_sum, k_win, v_win
     resident forced windows and the routed groups read from host memory."""
     B, H, L, d = cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim
     dt, kvt = cfg.torch_dtype(), cfg.kv_torch_dtype()
-    win = (B, H, window_slots(cfg) * cfg.chunk_size, d)
+    win = cfg.kv_rows(B, H, rows=window_slots(cfg) * cfg.chunk_size)
+    store = cfg.kv_rows(B, H, rows=L)
     r = _route_ptrs(cfg, q_rot, chunk_sum, group_sum, qbar, sel_chunks, n_sel_chunks, sel_groups,
                     n_sel_groups)
     _check(_lib.hga_decode_step_tiered(
         ctypes.byref(cfg), r[0], r[1], r[2], _ptr(k_win, "k_win", kvt, win),
-        _ptr(v_win, "v_win", kvt, win), _ptr(k_host, "k_host", kvt, (B, H, L, d), device=False),
-        _ptr(v_host, "v_host", kvt, (B, H, L, d), device=False), *r[3:],
+        _ptr(v_win, "v_win", kvt, win), _ptr(k_host, "k_host", kvt, store, device=False),
+        _ptr(v_host, "v_host", kvt, store, device=False), *r[3:],
         _ptr(out, "out", dt, (B, cfg.q_len, cfg.n_q_heads, d)), _stream(stream)),
         "hga_decode_step_tiered")
 
@@ -299,10 +413,11 @@ def gather_kv(cfg: HgaConfig, k_src, v_src, src_is_host: bool, sel_groups, n_sel
               v_dst, stream=None) -> None:
     B, H, L, d, nQC = cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_qchunks
     dt = cfg.kv_torch_dtype()
-    dst_shape = (B, H, nQC, cfg.top_k_groups * cfg.group_size, d)
+    dst_shape = cfg.kv_rows(B, H, nQC, rows=cfg.top_k_groups * cfg.group_size)
+    store = cfg.kv_rows(B, H, rows=L)
     _check(_lib.hga_gather_kv(
-        ctypes.byref(cfg), _ptr(k_src, "k_src", dt, (B, H, L, d), device=not src_is_host),
-        _ptr(v_src, "v_src", dt, (B, H, L, d), device=not src_is_host), int(bool(src_is_host)),
+        ctypes.byref(cfg), _ptr(k_src, "k_src", dt, store, device=not src_is_host),
+        _ptr(v_src, "v_src", dt, store, device=not src_is_host), int(bool(src_is_host)),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, H, nQC, cfg.top_k_groups)),
         _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, H, nQC)),
         _ptr(k_dst, "k_dst", dt, dst_shape), _ptr(v_dst, "v_dst", dt, dst_shape),
@@ -316,15 +431,15 @@ def gather_kv_warm(cfg: HgaConfig, k_host, v_host, sel_groups, n_sel_groups, poo
     B, H, d, kg, g = cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.top_k_groups, cfg.group_size
     dt = cfg.kv_torch_dtype()
     n_slots = pool_tag.shape[-1]
-    store = (B, H, cfg.seq_len, d)
-    gat_shape = (B, H, cfg.n_qchunks, kg * g, d)
+    store = cfg.kv_rows(B, H, rows=cfg.seq_len)
+    gat_shape = cfg.kv_rows(B, H, cfg.n_qchunks, rows=kg * g)
+    pool = pool_shape(cfg, n_slots)
     _check(_lib.hga_gather_kv_warm(
         ctypes.byref(cfg), _ptr(k_host, "k_host", dt, store, device=False),
         _ptr(v_host, "v_host", dt, store, device=False),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, H, cfg.n_qchunks, kg)),
         _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, H, cfg.n_qchunks)),
-        _ptr(pool_k, "pool_k", dt, (B, H, n_slots, g, d)),
-        _ptr(pool_v, "pool_v", dt, (B, H, n_slots, g, d)),
+        _ptr(pool_k, "pool_k", dt, pool), _ptr(pool_v, "pool_v", dt, pool),
         _ptr(pool_tag, "pool_tag", torch.int32, (B, H, n_slots)),
         _ptr(pool_last, "pool_last", torch.int32, (B, H, n_slots)), n_slots, step,
         _ptr(src_out, "src_out", torch.int32, (B, H, kg)),
@@ -342,20 +457,27 @@ def gather_kv_warm_noalloc(cfg: HgaConfig, k_host, v_host, sel_groups, n_sel_gro
     B, H, d, kg, g = cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.top_k_groups, cfg.group_size
     dt = cfg.kv_torch_dtype()
     n_slots = pool_tag.shape[-1]
-    store = (B, H, cfg.seq_len, d)
-    gat_shape = (B, H, cfg.n_qchunks, kg * g, d)
+    store = cfg.kv_rows(B, H, rows=cfg.seq_len)
+    gat_shape = cfg.kv_rows(B, H, cfg.n_qchunks, rows=kg * g)
+    pool = pool_shape(cfg, n_slots)
     _check(_lib.hga_gather_kv_warm_noalloc(
         ctypes.byref(cfg), _ptr(k_host, "k_host", dt, store, device=False),
         _ptr(v_host, "v_host", dt, store, device=False),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, H, cfg.n_qchunks, kg)),
         _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, H, cfg.n_qchunks)),
-        _ptr(pool_k, "pool_k", dt, (B, H, n_slots, g, d)),
-        _ptr(pool_v, "pool_v", dt, (B, H, n_slots, g, d)),
+        _ptr(pool_k, "pool_k", dt, pool), _ptr(pool_v, "pool_v", dt, pool),
         _ptr(pool_tag, "pool_tag", torch.int32, (B, H, n_slots)),
         _ptr(pool_last, "pool_last", torch.int32, (B, H, n_slots)), n_slots, step,
         _ptr(stats, "stats", torch.int32, (B, H, 2), nullable=True),
         _ptr(k_dst, "k_dst", dt, gat_shape), _ptr(v_dst, "v_dst", dt, gat_shape),
         _stream(stream)), "hga_gather_kv_warm_noalloc")
+
+
+def pool_shape(cfg: HgaConfig, n_slots: int) -> tuple:
+    """Shape of a warm tier's key or value pool."""
+    lead = (cfg.batch, cfg.n_kv_heads, n_slots)
+    return (*lead, HGA_E2M1_PAGE) if cfg.kv_type == HGA_KV_E2M1 else (
+        *lead, cfg.group_size, cfg.head_dim)
 
 
 def window_slots(cfg: HgaConfig) -> int:
@@ -368,12 +490,12 @@ def attend(cfg: HgaConfig, q_rot, k_res, v_res, sel_groups, n_sel_groups, out, k
     B, H, L, d, nQC = cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_qchunks
     dt, kvt = cfg.torch_dtype(), cfg.kv_torch_dtype()
     res_len = L if cfg.kv_layout == HGA_KV_FULL else window_slots(cfg) * cfg.chunk_size
-    gat_shape = (B, H, nQC, cfg.top_k_groups * cfg.group_size, d)
+    gat_shape = cfg.kv_rows(B, H, nQC, rows=cfg.top_k_groups * cfg.group_size)
+    res_shape = cfg.kv_rows(B, H, rows=res_len)
     q_shape = (B, cfg.q_len, cfg.n_q_heads, d)
     _check(_lib.hga_attend(
         ctypes.byref(cfg), _ptr(q_rot, "q_rot", dt, q_shape),
-        _ptr(k_res, "k_res", kvt, (B, H, res_len, d)),
-        _ptr(v_res, "v_res", kvt, (B, H, res_len, d)),
+        _ptr(k_res, "k_res", kvt, res_shape), _ptr(v_res, "v_res", kvt, res_shape),
         _ptr(k_gat, "k_gat", kvt, gat_shape, nullable=True),
         _ptr(v_gat, "v_gat", kvt, gat_shape, nullable=True),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, cfg.route_heads, nQC, cfg.top_k_groups)),

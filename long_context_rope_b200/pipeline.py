@@ -47,11 +47,12 @@ class WarmPool:
 
 
 def alloc_warm_pool(cfg: hga.HgaConfig, n_slots: int, device="cuda") -> WarmPool:
-    B, H, d, g = cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.group_size
+    B, H = cfg.batch, cfg.n_kv_heads
     i32 = dict(dtype=torch.int32, device=device)
+    pool = hga.pool_shape(cfg, n_slots)
     return WarmPool(
-        k=torch.zeros(B, H, n_slots, g, d, dtype=cfg.kv_torch_dtype(), device=device),
-        v=torch.zeros(B, H, n_slots, g, d, dtype=cfg.kv_torch_dtype(), device=device),
+        k=torch.zeros(pool, dtype=cfg.kv_torch_dtype(), device=device),
+        v=torch.zeros(pool, dtype=cfg.kv_torch_dtype(), device=device),
         tag=torch.full((B, H, n_slots), -1, **i32), last=torch.full((B, H, n_slots), -1, **i32),
         src=torch.empty(B, H, cfg.top_k_groups, **i32), stats=torch.zeros(B, H, 2, **i32))
 
@@ -81,20 +82,42 @@ def alloc_route(cfg: hga.HgaConfig, device="cuda", with_scores: bool = False) ->
 
 
 def alloc_gathered(cfg: hga.HgaConfig, device="cuda"):
-    shape = (cfg.batch, cfg.n_kv_heads, cfg.n_qchunks, cfg.top_k_groups * cfg.group_size,
-             cfg.head_dim)
+    shape = cfg.kv_rows(cfg.batch, cfg.n_kv_heads, cfg.n_qchunks,
+                        rows=cfg.top_k_groups * cfg.group_size)
     return (torch.zeros(shape, dtype=cfg.kv_torch_dtype(), device=device),
             torch.zeros(shape, dtype=cfg.kv_torch_dtype(), device=device))
 
 
-def rotate_queries(cfg: hga.HgaConfig, q_raw: torch.Tensor, stream=None) -> torch.Tensor:
+def alloc_store(cfg: hga.HgaConfig, device="cuda"):
+    """Key and value stores of cfg's kv_type, zeroed: [B, Hkv, L, d], or pages."""
+    shape = cfg.kv_rows(cfg.batch, cfg.n_kv_heads, rows=cfg.seq_len)
+    return (torch.zeros(shape, dtype=cfg.kv_torch_dtype(), device=device),
+            torch.zeros(shape, dtype=cfg.kv_torch_dtype(), device=device))
+
+
+def rotate_queries(cfg: hga.HgaConfig, q_raw: torch.Tensor, stream=None, axes=None,
+                   positions=None) -> torch.Tensor:
+    """Rotate queries [B, q_len, Hq, d] by their token positions, or with axes by
+    positions [n_axes, B, q_len] int32."""
     q_rot = torch.empty_like(q_raw)
-    hga.apply_rope(cfg, q_raw, q_rot, cfg.batch, cfg.q_len, cfg.n_q_heads, cfg.q_begin, stream)
+    if axes is not None:
+        hga.apply_rope_axes(cfg, axes, positions, q_raw, q_rot, cfg.batch, cfg.q_len, cfg.n_q_heads,
+                            stream)
+    else:
+        hga.apply_rope(cfg, q_raw, q_rot, cfg.batch, cfg.q_len, cfg.n_q_heads, cfg.q_begin, stream)
     return q_rot
 
 
-def summaries(cfg: hga.HgaConfig, k_raw, cs, gs, k_rot=None, stream=None):
-    hga.build_summaries(cfg, k_raw, cs, gs, k_rot, 0, cfg.n_chunks, stream)
+def summaries(cfg: hga.HgaConfig, k_raw, cs, gs, k_rot=None, stream=None, axes=None,
+              positions=None, chunk_begin: int = 0, chunk_end: Optional[int] = None):
+    """Key summaries (and rotated keys) of chunks [chunk_begin, chunk_end), by token
+    position or with axes by positions [n_axes, B, L] int32."""
+    chunk_end = cfg.n_chunks if chunk_end is None else chunk_end
+    if axes is not None:
+        hga.build_summaries_axes(cfg, axes, positions, k_raw, cs, gs, k_rot, chunk_begin, chunk_end,
+                                 stream)
+    else:
+        hga.build_summaries(cfg, k_raw, cs, gs, k_rot, chunk_begin, chunk_end, stream)
 
 
 def route(cfg: hga.HgaConfig, q_rot, cs, gs, rb: RouteBuffers, stream=None,
@@ -113,10 +136,24 @@ def route(cfg: hga.HgaConfig, q_rot, cs, gs, rb: RouteBuffers, stream=None,
                   rb.n_sel_groups, stream)
 
 
+def _one_axis(cfg: hga.HgaConfig) -> hga.HgaRopeAxes:
+    """Every pair on one axis: the token position."""
+    return hga.rope_axes([0] * (cfg.head_dim // 2), 1)
+
+
 def prefill(cfg: hga.HgaConfig, k_raw, v, q_rot, cs, gs, k_rot, rb: RouteBuffers, out,
-            stream=None):
-    """One pass of the prefill hot path (summaries, routing, attention)."""
-    summaries(cfg, k_raw, cs, gs, k_rot, stream)
+            stream=None, v_store=None, axes=None, positions=None):
+    """One pass of the prefill hot path (summaries, routing, attention).
+
+    With kv_type E2M1, k_rot and v_store are the 4-bit stores, which the pass
+    fills (hga_store_kv, the keys rotated on the way) and attends over. axes
+    and positions [n_axes, B, L]: rotary positions with several axes."""
+    if cfg.kv_type == hga.HGA_KV_E2M1:
+        summaries(cfg, k_raw, cs, gs, None, stream, axes, positions)
+        hga.store_kv(cfg, k_raw, v, k_rot, v_store, 0, axes or _one_axis(cfg), positions, stream)
+        v = v_store
+    else:
+        summaries(cfg, k_raw, cs, gs, k_rot, stream, axes, positions)
     route(cfg, q_rot, cs, gs, rb, stream)
     hga.attend(cfg, q_rot, k_rot, v, rb.sel_groups, rb.n_sel_groups, out, stream=stream)
 
@@ -171,15 +208,17 @@ def forced_window_chunks(cfg: hga.HgaConfig):
 def fill_windows(cfg: hga.HgaConfig, k_full, v_full, k_win, v_win):
     """Copy the forced chunks of the decode query chunk from the full store
     (host or device) into the resident window buffers (device). Copies only."""
-    C = cfg.chunk_size
+    # rows per chunk and in all: tokens, or pages of the 4-bit store
+    C, L = cfg.kv_rows(rows=cfg.chunk_size)[0], cfg.kv_rows(rows=cfg.seq_len)[0]
     for w, c in enumerate(forced_window_chunks(cfg)):
-        hi = min((c + 1) * C, cfg.seq_len)
+        hi = min((c + 1) * C, L)
         k_win[:, :, w * C: w * C + hi - c * C].copy_(k_full[:, :, c * C: hi], non_blocking=True)
         v_win[:, :, w * C: w * C + hi - c * C].copy_(v_full[:, :, c * C: hi], non_blocking=True)
 
 
 def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new, k_raw_cache,
-                  k_rot_cache, v_cache, cs, gs, rb: RouteBuffers, out, stream=None):
+                  k_rot_cache, v_cache, cs, gs, rb: RouteBuffers, out, stream=None, axes=None,
+                  positions=None):
     """One step of a decode loop over caches of fixed capacity cfg_cap.seq_len
     ([B, Hkv, capacity, d]) at token position `pos`.
 
@@ -190,17 +229,32 @@ def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new,
     attends for the query q_rot_new [B, 1, Hq, d] at position pos
     (hga_decode_step with q_begin = pos, q_len = 1): routing reads only the
     summaries of chunks before the query's chunk, and attention masks keys
-    after pos, so cache rows past pos are never used."""
+    after pos, so cache rows past pos are never used.
+
+    With axes, the key turns by positions[:, :, pos] of positions
+    [n_axes, B, capacity] int32 instead. With kv_type E2M1, k_rot_cache and
+    v_cache are 4-bit stores and the token goes into both in one launch
+    (hga_store_kv)."""
     B, H, d = cfg_cap.batch, cfg_cap.n_kv_heads, cfg_cap.head_dim
     k_new_raw = k_new_raw.contiguous()
+    at = None if positions is None else positions[:, :, pos:pos + 1].contiguous()
     k_raw_cache[:, :, pos].copy_(k_new_raw, non_blocking=True)
-    v_cache[:, :, pos].copy_(v_new, non_blocking=True)
-    rot = torch.empty_like(k_new_raw)
-    hga.apply_rope(cfg_cap, k_new_raw, rot, B * H, 1, 1, pos, stream)
-    k_rot_cache[:, :, pos].copy_(rot, non_blocking=True)
+    rot_cache = k_rot_cache
+    if cfg_cap.kv_type == hga.HGA_KV_E2M1:
+        hga.store_kv(cfg_cap, k_new_raw.unsqueeze(2), v_new.contiguous().unsqueeze(2), k_rot_cache,
+                     v_cache, pos, axes or _one_axis(cfg_cap), at, stream)
+        rot_cache = None
+    else:
+        v_cache[:, :, pos].copy_(v_new, non_blocking=True)
+        rot = torch.empty_like(k_new_raw)
+        if axes is not None:
+            hga.apply_rope_axes(cfg_cap, axes, at, k_new_raw, rot, B * H, 1, 1, stream)
+        else:
+            hga.apply_rope(cfg_cap, k_new_raw, rot, B * H, 1, 1, pos, stream)
+        k_rot_cache[:, :, pos].copy_(rot, non_blocking=True)
     if (pos + 1) % cfg_cap.chunk_size == 0:
         c = pos // cfg_cap.chunk_size
-        hga.build_summaries(cfg_cap, k_raw_cache, cs, gs, k_rot_cache, c, c + 1, stream)
+        summaries(cfg_cap, k_raw_cache, cs, gs, rot_cache, stream, axes, positions, c, c + 1)
     cfg_q = cfg_cap.copy(q_begin=pos, q_len=1)
     hga.decode_step(cfg_q, q_rot_new, cs, gs, k_rot_cache, v_cache, rb.qbar, rb.sel_chunks,
                     rb.n_sel_chunks, rb.sel_groups, rb.n_sel_groups, out, stream)
@@ -241,6 +295,8 @@ class HostPrefill:
     def __init__(self, cfg: hga.HgaConfig, chunks_per_slice: int = 64, device="cuda"):
         if cfg.q_begin % cfg.chunk_size != 0:
             raise ValueError("HostPrefill: the span must start on a chunk boundary")
+        if cfg.kv_type == hga.HGA_KV_E2M1:
+            raise ValueError("HostPrefill: keys and values in dtype only")
         self.cfg = cfg
         B, L, Hq, d = cfg.batch, cfg.q_len, cfg.n_q_heads, cfg.head_dim
         dt = cfg.kv_torch_dtype()
