@@ -70,6 +70,18 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// An f16 pair times the low (half 0) or high (half 1) element of c.
+__device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t c, int half) {
+    const __half2 c2 = *reinterpret_cast<const __half2*>(&c);
+    const __half2 d = half ? __high2half2(c2) : __low2half2(c2);
+    return hmul2(a, *reinterpret_cast<const uint32_t*>(&d));
+}
+
+// The low half of every byte of a, and the high half of every byte of b.
+__device__ __forceinline__ uint32_t select_low_nibbles(uint32_t a, uint32_t b) {
+    return (a & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+}
+
 // Sixteen elements of one block: their codes and the block's scale code, by
 // the rounding that hga_store_kv states. `ts` is the tensor scale. The divide
 // is the correctly rounded one: of bf16 elements and a power-of-two ts the

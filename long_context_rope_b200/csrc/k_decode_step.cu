@@ -61,10 +61,6 @@ constexpr int kMaxLocal = 256;   // key blocks per CTA
 constexpr int kRankThreads = kConsumers * 32;
 constexpr int kL1Rows = 16;      // level-1 rows per consumer warp per batch
 
-struct StepMaps {
-    CUtensorMap k, v;
-};
-
 struct StepSmem {
     union {
         dec::Ring ring;
@@ -190,26 +186,33 @@ __device__ __forceinline__ void score_rows(const float* q, int n, RowOf row_of, 
 // link with 16-byte loads (each lane 8 (bf16) or 4 (E4M3) of each tensor,
 // 512 contiguous bytes per warp load) and stored into ring stage s in the
 // layout the TMA tile loads write: 128-byte panels of 16 rows (two for bf16,
-// one for E4M3), 16-byte chunk c of row r at c ^ (r % 8).
-template <bool kF8>
+// one for E4M3), 16-byte chunk c of row r at c ^ (r % 8). An E2M1 group is
+// one page of 72 pieces and is copied as it is.
+template <int kKv>
 __device__ __forceinline__ void copy_host_block(dec::Ring& ring, int s, const uint4* kh,
                                                 const uint4* vh) {
     const int lane = threadIdx.x & 31;
-    constexpr int kPieces = kF8 ? 4 : 8;             // per lane per tensor
-    constexpr int kRowPieces = kF8 ? 8 : 16;         // 16-byte pieces per row
+    constexpr int kVecs = dec::blk_bytes<kKv>() / 16;
+    constexpr int kPieces = (kVecs + 31) / 32;       // per lane per tensor
+    constexpr int kRowPieces = kKv == dec::kKvE4m3 ? 8 : 16;  // 16-byte pieces per row
     uint4 kr[kPieces], vr[kPieces];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-        kr[u] = kh[lane + 32 * u];
-        vr[u] = vh[lane + 32 * u];
+        if (kVecs % 32 == 0 || lane + 32 * u < kVecs) {
+            kr[u] = kh[lane + 32 * u];
+            vr[u] = vh[lane + 32 * u];
+        }
     }
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
         const int idx = lane + 32 * u;               // 16-byte piece of the block
+        if (kVecs % 32 != 0 && idx >= kVecs) break;
         const int row = idx / kRowPieces, c16 = idx % kRowPieces;
-        const int off = (c16 >> 3) * 2048 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(dec::k_stage<kF8>(ring, s) + off) = kr[u];
-        *reinterpret_cast<uint4*>(dec::v_stage<kF8>(ring, s) + off) = vr[u];
+        const int off = kKv == dec::kKvE2m1
+                            ? idx * 16
+                            : (c16 >> 3) * 2048 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(dec::k_stage<kKv>(ring, s) + off) = kr[u];
+        *reinterpret_cast<uint4*>(dec::v_stage<kKv>(ring, s) + off) = vr[u];
     }
     // a later tile load into this stage (async proxy) is ordered after these
     // stores
@@ -217,14 +220,14 @@ __device__ __forceinline__ void copy_host_block(dec::Ring& ring, int s, const ui
 }
 
 // S: element type of the summary tables (float, or bf16 for bf16 tables).
-// kF8: keys and values are E4M3 codes (else bf16).
+// kKv: how keys and values are stored (hga_decode_core.cuh).
 // k_host / v_host: nullptr, or the full store [B, Hkv, L, d] in mapped host
-// memory (the host tier); then the maps cover the resident windows of the
+// memory (the host tier); then src covers the resident windows of the
 // forced chunks ([B, Hkv, W * C, d]) and the routed groups are read from the
 // host by the producer warp.
-template <typename S, bool kF8>
+template <typename S, int kKv>
 __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
-    const __grid_constant__ StepMaps maps, Params p, const __nv_bfloat16* __restrict__ q,
+    const __grid_constant__ dec::Source<kKv> src, Params p, const __nv_bfloat16* __restrict__ q,
     const S* __restrict__ cs, const S* __restrict__ gs, float* __restrict__ qbar_out,
     int32_t* __restrict__ sel_c, int32_t* __restrict__ nsel_c, int32_t* __restrict__ sel_g,
     int32_t* __restrict__ nsel_g, __nv_bfloat16* __restrict__ out, int attend,
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
         sm.blk_row[i] = host_tier ? w * p.C + kGroupRows * gm : sm.blk_pos[i];
     }
     __syncthreads();
-    constexpr int kS = dec::ring_stages<kF8>();
+    constexpr int kS = dec::ring_stages<kKv>();
     const int n_pre = nf_loc < kS ? nf_loc : kS;
 
     // ---- level-1 slice: the first batch of this warp's chunk-summary rows is
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
     // on the critical path
     if (attend && warp == kConsumers && lane == 0)
         for (int i = 0; i < n_pre; ++i)
-            dec::issue_block<kF8>(sm.u.ring, sm.full, i, &maps.k, &maps.v, sm.blk_row[i], (int)kvh);
+            dec::issue_block<kKv>(sm.u.ring, sm.full, i, src, sm.blk_row[i], kvh);
     // this CTA's winners, in candidate (= ascending chunk) order, padded
     // with 0 to cap1 entries. (Prefetching the winners' group rows into L2
     // here, with one bulk prefetch per winner, cost more in this phase than
@@ -454,13 +457,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
                 }
             }
             if (host_tier && i >= nf_loc) {
-                const int64_t row = kvh * (int64_t)p.L + sm.blk_row[i];
-                constexpr int kRowVecs = kF8 ? kD / 16 : kD / 8;  // 16-byte pieces per row
-                copy_host_block<kF8>(sm.u.ring, s, k_host + row * kRowVecs, v_host + row * kRowVecs);
+                // blocks of 16 rows lie one after another in a unit's slab
+                const int64_t at = kvh * (p.kv_slab / 16) +
+                                   (int64_t)(sm.blk_row[i] / kGroupRows) * (dec::blk_bytes<kKv>() / 16);
+                copy_host_block<kKv>(sm.u.ring, s, k_host + at, v_host + at);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&sm.full[s]);
             } else if (lane == 0) {
-                dec::issue_block<kF8>(sm.u.ring, sm.full, s, &maps.k, &maps.v, sm.blk_row[i], (int)kvh);
+                dec::issue_block<kKv>(sm.u.ring, sm.full, s, src, sm.blk_row[i], kvh);
             }
         }
         if (lane == 0) {
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
             }
             // every issued load (the early forced blocks included) lands
             // before the ring's memory is reused
-            if (!dec::drain_ring<kF8>(sm.full, i)) {
+            if (!dec::drain_ring<kKv>(sm.full, i)) {
                 raise_timeout(p);
                 sm.bad = 1;
             }
@@ -480,12 +484,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
     dec::acc_init(acc);
     if (consumer) {
         uint32_t qf[8][2];
-        dec::load_q_frags<kF8>(p, q, b, h, qf);
-        dec::consume_blocks<kF8>(p, qf, sm.u.ring, sm.full, sm.empty, sm.blk_pos, nloc, p.q_begin,
+        float sc[2];
+        dec::load_q_frags<kKv>(p, q, b, h, qf, sc);
+        dec::consume_blocks<kKv>(p, qf, sc, sm.u.ring, sm.full, sm.empty, sm.blk_pos, nloc, p.q_begin,
                             sm.pt[warp], acc, &sm.bad);
     }
     __syncthreads();
-    if (consumer) dec::store_warp_partial<kF8>(acc, sm.u.warp_part[warp]);
+    if (consumer) dec::store_warp_partial<kKv>(acc, sm.u.warp_part[warp]);
     __syncthreads();
     dec::merge_warps_push(sm.u.warp_part, cluster, sm.owned, sm.wgt, p.gq);
     cluster.sync();  // every partial is in its owner's shared memory
@@ -506,26 +511,26 @@ bool step_fits(const Params& p, int cl) {
 
 std::mutex g_step_mu;
 // per device, summary type and K/V type, 0 = not queried
-int g_max_active[kMaxDevicesPerProcess][2][2][kMaxCluster + 1] = {};
+int g_max_active[kMaxDevicesPerProcess][2][3][kMaxCluster + 1] = {};
 
-template <typename S, bool kF8>
+template <typename S, int kKv>
 cudaError_t step_prepare(size_t smem) {
-    cudaError_t e = set_func_attr_once((const void*)decode_step_kernel<S, kF8>,
+    cudaError_t e = set_func_attr_once((const void*)decode_step_kernel<S, kKv>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-        e = set_func_attr_once((const void*)decode_step_kernel<S, kF8>,
+        e = set_func_attr_once((const void*)decode_step_kernel<S, kKv>,
                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;
 }
 
 // Clusters of `cl` CTAs that can be resident at once on the current device
 // (-1 if the query fails).
-template <typename S, bool kF8>
+template <typename S, int kKv>
 int active_clusters(int cl, size_t smem) {
     int dev = 0;
     if (current_device_index(&dev) != cudaSuccess) return -1;
     std::lock_guard<std::mutex> lock(g_step_mu);
-    int& slot = g_max_active[dev][sizeof(S) == 2 ? 1 : 0][kF8 ? 1 : 0][cl];
+    int& slot = g_max_active[dev][sizeof(S) == 2 ? 1 : 0][kKv][cl];
     if (slot == 0) {
         cudaLaunchConfig_t q = {};
         q.gridDim = dim3(cl, 1, 1);
@@ -539,7 +544,7 @@ int active_clusters(int cl, size_t smem) {
         q.attrs = a;
         q.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, decode_step_kernel<S, kF8>, &q) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, decode_step_kernel<S, kKv>, &q) != cudaSuccess) {
             cudaGetLastError();
             n = -1;
         }
@@ -550,7 +555,7 @@ int active_clusters(int cl, size_t smem) {
 
 // Cluster size: two CTAs per SM over the whole grid if the tables fit and the
 // clusters can all be resident at once; else the largest size that fits.
-template <typename S, bool kF8>
+template <typename S, int kKv>
 int step_cluster(const Params& p, size_t smem) {
     int sms = 148, dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess)
@@ -561,7 +566,7 @@ int step_cluster(const Params& p, size_t smem) {
     for (; cl >= 1; --cl) {
         if (!step_fits(p, cl)) continue;
         if (cl == 1) return 1;
-        const int n = active_clusters<S, kF8>(cl, smem);
+        const int n = active_clusters<S, kKv>(cl, smem);
         if (n >= units || (n > 0 && cl <= 2)) return cl;
     }
     return 0;
@@ -570,8 +575,8 @@ int step_cluster(const Params& p, size_t smem) {
 }  // namespace
 
 bool decode_step_supports(const Params& p) {
-    if (!(!p.kv_f4 && p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.gq <= 8 && p.L % kGroupRows == 0 &&
-          p.kc <= kMaxKc && p.kg <= kMaxKg && p.nQC == 1))
+    if (!(p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.gq <= 8 &&
+          (p.kv_f4 || p.L % kGroupRows == 0) && p.kc <= kMaxKc && p.kg <= kMaxKg && p.nQC == 1))
         return false;
     for (int cl = 1; cl <= kMaxCluster; ++cl)
         if (step_fits(p, cl)) return true;
@@ -580,31 +585,36 @@ bool decode_step_supports(const Params& p) {
 
 namespace {
 
-template <typename S, bool kF8>
+template <typename S, int kKv>
 cudaError_t launch_step(const Params& p, const void* q_rot, const S* chunk_sum,
                         const S* group_sum, const void* k_cache, const void* v_cache, float* qbar,
                         int32_t* sel_chunks, int32_t* n_sel_chunks, int32_t* sel_groups,
                         int32_t* n_sel_groups, void* out, const void* k_host, const void* v_host,
                         cudaStream_t st) {
     const bool attend = out != nullptr;
-    StepMaps maps;
+    dec::Source<kKv> src;
+    memset(&src, 0, sizeof(src));
     if (attend) {
         const int64_t BH = (int64_t)p.B * p.Hkv;
         const int64_t rows = p.kv_layout == HGA_KV_WINDOWS
                                  ? (int64_t)(p.n_sink + p.n_local + 1) * p.C
                                  : (int64_t)p.L;
-        const bool ok = kF8 ? make_rows_map_u8(&maps.k, k_cache, BH, rows, kD, kGroupRows) &&
-                                  make_rows_map_u8(&maps.v, v_cache, BH, rows, kD, kGroupRows)
-                            : make_rows_map(&maps.k, k_cache, BH, rows, kD, kGroupRows) &&
-                                  make_rows_map(&maps.v, v_cache, BH, rows, kD, kGroupRows);
+        bool ok = true;
+        if constexpr (kKv == dec::kKvE2m1)
+            src = {(const uint8_t*)k_cache, (const uint8_t*)v_cache,
+                   (rows + kGroupRows - 1) / kGroupRows * kE2m1Page};
+        else if constexpr (kKv == dec::kKvE4m3)
+            ok = make_rows_map_u8(&src.k, k_cache, BH, rows, kD, kGroupRows) &&
+                 make_rows_map_u8(&src.v, v_cache, BH, rows, kD, kGroupRows);
+        else
+            ok = make_rows_map(&src.k, k_cache, BH, rows, kD, kGroupRows) &&
+                 make_rows_map(&src.v, v_cache, BH, rows, kD, kGroupRows);
         if (!ok) return cudaErrorInvalidValue;
-    } else {
-        memset(&maps, 0, sizeof(maps));
     }
     const size_t smem = sizeof(StepSmem) + 1024;
-    cudaError_t e = step_prepare<S, kF8>(smem);
+    cudaError_t e = step_prepare<S, kKv>(smem);
     if (e != cudaSuccess) return e;
-    const int cl = step_cluster<S, kF8>(p, smem);
+    const int cl = step_cluster<S, kKv>(p, smem);
     if (cl < 1) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cl, (unsigned)(p.B * p.Hu), 1);
@@ -618,7 +628,7 @@ cudaError_t launch_step(const Params& p, const void* q_rot, const S* chunk_sum,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_step_kernel<S, kF8>, maps, p, (const __nv_bfloat16*)q_rot,
+    return cudaLaunchKernelEx(&cfg, decode_step_kernel<S, kKv>, src, p, (const __nv_bfloat16*)q_rot,
                               chunk_sum, group_sum, qbar, sel_chunks, n_sel_chunks, sel_groups,
                               n_sel_groups, (__nv_bfloat16*)out, attend ? 1 : 0,
                               (const uint4*)k_host, (const uint4*)v_host);
@@ -632,22 +642,18 @@ cudaError_t launch_decode_step(const Params& p, const void* q_rot, const void* c
                                int32_t* sel_groups, int32_t* n_sel_groups, void* out,
                                cudaStream_t st, const void* k_host, const void* v_host) {
     using bf = __nv_bfloat16;
-    const bf* cb = (const bf*)chunk_sum;
-    const bf* gb = (const bf*)group_sum;
-    const float* cf = (const float*)chunk_sum;
-    const float* gf = (const float*)group_sum;
-    if (p.sum_bf16 && p.kv_f8)
-        return launch_step<bf, true>(p, q_rot, cb, gb, k_cache, v_cache, qbar, sel_chunks,
-                                     n_sel_chunks, sel_groups, n_sel_groups, out, k_host, v_host, st);
-    if (p.sum_bf16)
-        return launch_step<bf, false>(p, q_rot, cb, gb, k_cache, v_cache, qbar, sel_chunks,
-                                      n_sel_chunks, sel_groups, n_sel_groups, out, k_host, v_host, st);
-    if (p.kv_f8)
-        return launch_step<float, true>(p, q_rot, cf, gf, k_cache, v_cache, qbar, sel_chunks,
-                                        n_sel_chunks, sel_groups, n_sel_groups, out, k_host, v_host,
-                                        st);
-    return launch_step<float, false>(p, q_rot, cf, gf, k_cache, v_cache, qbar, sel_chunks,
-                                     n_sel_chunks, sel_groups, n_sel_groups, out, k_host, v_host, st);
+    auto run = [&](auto s, auto kv) {
+        using S = decltype(s);
+        return launch_step<S, decltype(kv)::value>(
+            p, q_rot, (const S*)chunk_sum, (const S*)group_sum, k_cache, v_cache, qbar, sel_chunks,
+            n_sel_chunks, sel_groups, n_sel_groups, out, k_host, v_host, st);
+    };
+    auto by_kv = [&](auto s) {
+        if (p.kv_f4) return run(s, std::integral_constant<int, dec::kKvE2m1>());
+        if (p.kv_f8) return run(s, std::integral_constant<int, dec::kKvE4m3>());
+        return run(s, std::integral_constant<int, dec::kKvBf16>());
+    };
+    return p.sum_bf16 ? by_kv(bf()) : by_kv(float());
 }
 
 }  // namespace hga
