@@ -28,31 +28,11 @@
 //               dim 64 + 8g + mt.
 // Both are bijections of the 128 dims, so the results are the same dot
 // products and output dims, in another summation order.
-//
-// E2M1 (4-bit) keys and values: a 16-row block is one page of 1152 bytes per
-// tensor, contiguous in memory, so it is one bulk copy. The products run on
-// fp16 MMA as for E4M3: code x block scale has at most 6 significant bits and
-// is exact in fp16. Shared-memory reads are 8x8 matrix loads of 16-bit
-// elements, four codes each:
-//   keys    plain: lane (g, t4) gets the 8 codes of row g, dims 32j + 8t4 ..
-//           +7 (two 8-row matrices per 32-dim tile j), the E4M3 permutation;
-//   values  transposed: lane (g, t4) gets the 4 codes of dims 32j + 4g .. +3
-//           of keys 2t4 (low half) and 2t4 + 1 (high half); two byte permutes
-//           and two shift-and-selects turn two such words into eight bytes
-//           that each hold one dim of both keys, the pair that one convert
-//           instruction widens. MMA tile 4a + e: output row g is dim
-//           64a + 4g + e and row g + 8 is dim 64a + 32 + 4g + e.
-// Queries are scaled per head by a power of two to at most 2^15 before they
-// are rounded to fp16, so bf16's whole range of queries is held (the inverse
-// goes into the score's factor).
 #pragma once
 
 #include <cooperative_groups.h>
 
-#include <type_traits>
-
 #include "hga_common.cuh"
-#include "hga_e2m1.cuh"
 #include "hga_ptx.cuh"
 
 namespace hga {
@@ -62,7 +42,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kD = 128;
 constexpr int kStages = 8;                       // ring of key blocks (bf16)
-constexpr int kStagesMax = 24;                   // E4M3: 16 blocks in the same bytes, E2M1: 24
+constexpr int kStagesMax = 16;                   // E4M3: the same bytes hold 16 blocks
 constexpr int kBlkBytes = kGroupRows * kD * 2;   // 4 KiB per block per tensor (bf16)
 constexpr int kBlkBytesF8 = kGroupRows * kD;     // 2 KiB per block per tensor (E4M3)
 constexpr int kConsumers = 8;                    // consumer warps
@@ -83,55 +63,28 @@ struct Ring {
     alignas(1024) uint8_t v[kStages][kBlkBytes];
 };
 
-// How keys and values are stored.
-constexpr int kKvBf16 = 0, kKvE4m3 = 1, kKvE2m1 = 2;
-
-// Ring geometry: 8 stages of 4 KiB per tensor (bf16), or in the same bytes 16
-// stages of 2 KiB (E4M3) or 24 of 1152 bytes (E2M1), so more of the smaller
-// blocks are in flight. A TMA tile's stage starts on a 1024-byte boundary (the
-// 128-byte swizzle's period), a page on a 128-byte one.
+// Ring geometry: 8 stages of 4 KiB per tensor (bf16), or 16 stages of 2 KiB
+// (E4M3) in the same bytes, so twice as many E4M3 blocks are in flight.
+// Every stage starts on a 1024-byte boundary (the 128-byte swizzle's period).
 // The stage count must be a multiple of the consumer warps: block i goes to
 // warp i % 8 and stage i % S, so every use of a stage then belongs to one
 // warp, which waits for its phases in order. With another count two warps
 // share a stage, and a warp that reaches its wait for phase k + 2 before
 // phase k + 1 has completed passes the parity wait at once (a parity names
 // only two phases) and reads a stage that is still being refilled.
-template <int kKv>
-__host__ __device__ constexpr int ring_stages() {
-    return kKv == kKvE2m1 ? 24 : kKv == kKvE4m3 ? 16 : kStages;
-}
-template <int kKv>
-__host__ __device__ constexpr int blk_bytes() {
-    return kKv == kKvE2m1 ? kE2m1Page : kKv == kKvE4m3 ? kBlkBytesF8 : kBlkBytes;
-}
-template <int kKv>
-constexpr bool ring_ok() {
-    return ring_stages<kKv>() % kConsumers == 0 && ring_stages<kKv>() <= kStagesMax &&
-           ring_stages<kKv>() * blk_bytes<kKv>() <= kStages * kBlkBytes;
-}
-static_assert(ring_ok<kKvBf16>() && ring_ok<kKvE4m3>() && ring_ok<kKvE2m1>(),
-              "ring stages must be a multiple of the consumer warps and fit the ring");
-template <int kKv>
+template <bool kF8>
+__host__ __device__ constexpr int ring_stages() { return kF8 ? kStagesMax : kStages; }
+static_assert(kStages % kConsumers == 0 && kStagesMax % kConsumers == 0,
+              "ring stages must be a multiple of the consumer warps");
+static_assert(kStagesMax * kBlkBytesF8 == kStages * kBlkBytes, "E4M3 stages fill the ring");
+template <bool kF8>
 __device__ __forceinline__ uint8_t* k_stage(Ring& ring, int s) {
-    return &ring.k[0][0] + s * blk_bytes<kKv>();
+    return &ring.k[0][0] + s * (kF8 ? kBlkBytesF8 : kBlkBytes);
 }
-template <int kKv>
+template <bool kF8>
 __device__ __forceinline__ uint8_t* v_stage(Ring& ring, int s) {
-    return &ring.v[0][0] + s * blk_bytes<kKv>();
+    return &ring.v[0][0] + s * (kF8 ? kBlkBytesF8 : kBlkBytes);
 }
-
-// Where blocks come from: TMA tiles of rows, or pages of E2M1 codes (`slab`
-// bytes from one sequence and KV head to the next).
-struct TileSource {
-    CUtensorMap k, v;
-};
-struct PageSource {
-    const uint8_t* k;
-    const uint8_t* v;
-    int64_t slab;
-};
-template <int kKv>
-using Source = std::conditional_t<kKv == kKvE2m1, PageSource, TileSource>;
 
 // Per-warp accumulator state of the online softmax.
 struct WarpAcc {
@@ -142,50 +95,25 @@ struct WarpAcc {
 // Q^T as MMA B fragments; heads >= gq are zero. bf16: lane (g, t4) holds
 // Q[head g][16kk + 2t4 .. +1] and Q[head g][16kk + 2t4 + 8 .. +9]. E4M3 path:
 // fp16 pairs of dims 32j + 8t4 + {0,1}, {2,3} (step 2j) and {4,5}, {6,7}
-// (step 2j + 1), the permutation the key fragments use; E2M1 the same, each
-// head scaled by a power of two. sc: the score factor of heads 2t4, 2t4 + 1
-// (log2 units).
-template <int kKv>
+// (step 2j + 1), the permutation the key fragments use.
+template <bool kF8>
 __device__ __forceinline__ void load_q_frags(const Params& p, const __nv_bfloat16* q, int b, int h,
-                                             uint32_t (&qf)[8][2], float (&sc)[2]) {
+                                             uint32_t (&qf)[8][2]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const bool okh = g < p.gq;
     const __nv_bfloat16* qr =
         q + ((int64_t)b * p.q_len * p.Hq + (int64_t)h * p.gq + (okh ? g : 0)) * kD;
-    const float sc0 = 1.4426950408889634f / sqrtf((float)kD);
-    sc[0] = sc[1] = kKv == kKvBf16 ? sc0 : sc0 * p.k_scale;
-    if constexpr (kKv != kKvBf16) {
-        uint4 raw[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            raw[j] = okh ? *reinterpret_cast<const uint4*>(qr + 32 * j + 8 * t4)
-                         : make_uint4(0u, 0u, 0u, 0u);
-        float up = 1.f;
-        if constexpr (kKv == kKvE2m1) {
-            // the head's largest exponent (bf16 bits 14..7), over its four lanes
-            uint32_t big = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                for (uint32_t w : {raw[j].x, raw[j].y, raw[j].z, raw[j].w})
-                    big = max(big, max((w >> 23) & 0xffu, (w >> 7) & 0xffu));
-            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // 2^(14 - e) for a largest exponent e = big - 127, from 2^-113 to
-            // 2^100; 1 for infinities and NaN
-            const int e = big == 255u ? 0 : min(141 - (int)big, 100);
-            up = __int_as_float((e + 127) << 23);
-            const float down = __int_as_float((127 - e) << 23);
-            sc[0] *= __shfl_sync(0xffffffffu, down, 8 * t4);
-            sc[1] *= __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
-        }
+    if constexpr (kF8) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&raw[j]);
+            const uint4 raw = okh ? *reinterpret_cast<const uint4*>(qr + 32 * j + 8 * t4)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+            const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&raw);
             uint32_t f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 v = __bfloat1622float2(h2[e]);
-                const __half2 hv = __floats2half2_rn(v.x * up, v.y * up);
+                const __half2 hv = __floats2half2_rn(v.x, v.y);
                 f[e] = *reinterpret_cast<const uint32_t*>(&hv);
             }
             qf[2 * j][0] = f[0];
@@ -221,17 +149,19 @@ __device__ __forceinline__ void acc_init(WarpAcc& a) {
 // the ring. blk_pos[i] is the position of block i's first token. pt is the
 // warp's 8 x 16 transpose buffer of P (bf16, or fp16 on the E4M3 path, as
 // bits). Returns false (and sets *bad) if a wait gave up.
-template <int kKv>
+template <bool kF8>
 __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (&qf)[8][2],
-                                               const float (&sc)[2], Ring& ring, uint64_t* full, uint64_t* empty,
+                                               Ring& ring, uint64_t* full, uint64_t* empty,
                                                const int* blk_pos, int nloc, int qpos,
                                                uint16_t (*pt)[16], WarpAcc& acc, int* bad) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
+    const float sc0 = 1.4426950408889634f / sqrtf((float)kD);
+    const float sc = kF8 ? sc0 * p.k_scale : sc0;
     const int mq = lane >> 3;
     const int krow = (mq & 1) * 8 + (lane & 7);      // K ldmatrix row
     const int vkey = (mq >> 1) * 8 + (lane & 7);     // V ldmatrix (trans) row
-    constexpr int S = ring_stages<kKv>();
+    constexpr int S = ring_stages<kF8>();
     for (int i = warp; i < nloc; i += kConsumers) {
         const int s = i % S;
         const bool got = __all_sync(
@@ -245,42 +175,10 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
         }
         // S^T = K Q^T for 16 keys x 8 heads (two accumulator chains)
         float sacc[4] = {0.f, 0.f, 0.f, 0.f}, sacc2[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (kKv == kKvE2m1) {
-            const uint8_t* kb = k_stage<kKv>(ring, s);
-            // the scales of rows g and g + 8; this lane's dims of tiles 2a and
-            // 2a + 1 are of blocks 4a + t4/2 and 4a + 2 + t4/2
-            const uint2 s0 = *reinterpret_cast<const uint2*>(kb + e2m1::scale_at(g, 0));
-            const uint2 s1 = *reinterpret_cast<const uint2*>(kb + e2m1::scale_at(g + 8, 0));
-            const unsigned pick = (unsigned)(t4 >> 1) * 0x11u + 0x20u;
-#pragma unroll
-            for (int a2 = 0; a2 < 2; ++a2) {
-                uint32_t w[4];
-                ptx::ldsm_x4(ptx::smem_u32(kb) + a2 * 512 + lane * 16, w);
-                const uint32_t c0 = e2m1::scales_to_f16x2(
-                    (uint16_t)__byte_perm(a2 ? s0.y : s0.x, 0u, pick));
-                const uint32_t c1 = e2m1::scales_to_f16x2(
-                    (uint16_t)__byte_perm(a2 ? s1.y : s1.x, 0u, pick));
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    const int j = 2 * a2 + tt;
-                    uint32_t f0[4], f1[4];
-                    e2m1::codes_to_f16x2(w[2 * tt], f0);
-                    e2m1::codes_to_f16x2(w[2 * tt + 1], f1);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f0[e] = e2m1::hmul2_half(f0[e], c0, tt);
-                        f1[e] = e2m1::hmul2_half(f1[e], c1, tt);
-                    }
-                    uint32_t a[4] = {f0[0], f1[0], f0[1], f1[1]};
-                    ptx::mma_16816_f16(sacc, a, qf[2 * j][0], qf[2 * j][1]);
-                    uint32_t b[4] = {f0[2], f1[2], f0[3], f1[3]};
-                    ptx::mma_16816_f16(sacc2, b, qf[2 * j + 1][0], qf[2 * j + 1][1]);
-                }
-            }
-        } else if constexpr (kKv == kKvE4m3) {
+        if constexpr (kF8) {
             // rows g and g + 8, dims 32j + 8t4 .. +7: 16-byte chunk 2j + t4/2
             // of the row, XOR-swizzled by the row (g and g + 8 alike)
-            const uint8_t* kb = k_stage<kKv>(ring, s);
+            const uint8_t* kb = k_stage<true>(ring, s);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int off = (((2 * j + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
@@ -298,7 +196,7 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
                 ptx::mma_16816_f16(sacc2, a2, qf[2 * j + 1][0], qf[2 * j + 1][1]);
             }
         } else {
-            const uint32_t kb = ptx::smem_u32(k_stage<kKv>(ring, s));
+            const uint32_t kb = ptx::smem_u32(k_stage<false>(ring, s));
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const int chunk = (kk & 3) * 2 + (mq >> 1);
@@ -312,16 +210,11 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
         // this lane holds keys g, g+8 for heads 2t4, 2t4+1
         const int kp = blk_pos[i];
         const bool v0 = kp + g <= qpos, v1 = kp + g + 8 <= qpos;
-        const float sv[4] = {v0 ? sacc[0] * sc[0] : -INFINITY, v0 ? sacc[1] * sc[1] : -INFINITY,
-                             v1 ? sacc[2] * sc[0] : -INFINITY, v1 ? sacc[3] * sc[1] : -INFINITY};
+        const float sv[4] = {v0 ? sacc[0] * sc : -INFINITY, v0 ? sacc[1] * sc : -INFINITY,
+                             v1 ? sacc[2] * sc : -INFINITY, v1 ? sacc[3] * sc : -INFINITY};
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             float mb = fmaxf(sv[hh], sv[hh + 2]);
-            if constexpr (kKv == kKvE2m1) {
-                // the maximum stays finite next to a NaN score (of a NaN scale),
-                // whose weight, and so its rows' output, is then NaN
-                if (isnan(sv[hh]) || isnan(sv[hh + 2])) mb = fmaxf(mb, 0.f);
-            }
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 4));
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
@@ -337,7 +230,7 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
             // same rounded values
             uint16_t b0, b1;
             float r0, r1;
-            if constexpr (kKv != kKvBf16) {
+            if constexpr (kF8) {
                 const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
                 b0 = __half_as_ushort(h0);
                 b1 = __half_as_ushort(h1);
@@ -363,58 +256,11 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
         const uint32_t pb0 = *reinterpret_cast<const uint32_t*>(&pt[g][2 * t4]);
         const uint32_t pb1 = *reinterpret_cast<const uint32_t*>(&pt[g][2 * t4 + 8]);
         // O^T[16 dims x 8 heads] += V^T P^T, eight 16-dim tiles
-        if constexpr (kKv == kKvE2m1) {
-            const uint8_t* vb = v_stage<kKv>(ring, s);
-            // the scales of keys 2t4, 2t4 + 1 and of keys 2t4 + 8, 2t4 + 9,
-            // 8 bytes a key; zero for keys after the query (their rows may
-            // hold anything)
-            uint4 sa = *reinterpret_cast<const uint4*>(vb + e2m1::scale_at(2 * t4, 0));
-            uint4 sb = *reinterpret_cast<const uint4*>(vb + e2m1::scale_at(2 * t4 + 8, 0));
-            if (kp + kGroupRows - 1 > qpos) {
-                if (kp + 2 * t4 > qpos) sa.x = sa.y = 0u;
-                if (kp + 2 * t4 + 1 > qpos) sa.z = sa.w = 0u;
-                if (kp + 2 * t4 + 8 > qpos) sb.x = sb.y = 0u;
-                if (kp + 2 * t4 + 9 > qpos) sb.z = sb.w = 0u;
-            }
-            // byte g/4 of word a of both keys: tile 2a; byte 2 + g/4: tile 2a + 1
-            const unsigned pick = 0x40u + (unsigned)(g >> 2) * 0x11u;
-#pragma unroll
-            for (int a2 = 0; a2 < 2; ++a2) {
-                uint32_t w[4];
-                ptx::ldsm_x4_trans(ptx::smem_u32(vb) + a2 * 512 + lane * 16, w);
-                uint32_t fe[2][4], fo[2][4];  // even and odd dims of keys 2t4.., 2t4 + 8..
-#pragma unroll
-                for (int kh = 0; kh < 2; ++kh) {
-                    const uint32_t x = __byte_perm(w[kh], w[2 + kh], 0x5410);  // first key's
-                    const uint32_t y = __byte_perm(w[kh], w[2 + kh], 0x7632);  // second key's
-                    e2m1::codes_to_f16x2(e2m1::select_low_nibbles(x, y << 4), fe[kh]);
-                    e2m1::codes_to_f16x2(e2m1::select_low_nibbles(x >> 4, y), fo[kh]);
-                    const uint4& sk = kh ? sb : sa;
-                    const uint32_t k0 = a2 ? sk.y : sk.x, k1 = a2 ? sk.w : sk.z;
-                    const uint32_t c0 = e2m1::scales_to_f16x2((uint16_t)__byte_perm(k0, k1, pick));
-                    const uint32_t c1 =
-                        e2m1::scales_to_f16x2((uint16_t)__byte_perm(k0, k1, pick + 0x22u));
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        fe[kh][e] = e2m1::hmul2(fe[kh][e], c0);
-                        fo[kh][e] = e2m1::hmul2(fo[kh][e], c0);
-                        fe[kh][2 + e] = e2m1::hmul2(fe[kh][2 + e], c1);
-                        fo[kh][2 + e] = e2m1::hmul2(fo[kh][2 + e], c1);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t ae[4] = {fe[0][e], fe[0][2 + e], fe[1][e], fe[1][2 + e]};
-                    ptx::mma_16816_f16(acc.o[4 * a2 + 2 * e], ae, pb0, pb1);
-                    uint32_t ao[4] = {fo[0][e], fo[0][2 + e], fo[1][e], fo[1][2 + e]};
-                    ptx::mma_16816_f16(acc.o[4 * a2 + 2 * e + 1], ao, pb0, pb1);
-                }
-            }
-        } else if constexpr (kKv == kKvE4m3) {
+        if constexpr (kF8) {
             // keys 2t4, 2t4 + 1, 2t4 + 8, 2t4 + 9; dims 8g .. +7 (rows g of
             // the tiles) and 64 + 8g .. +7 (rows g + 8): 16-byte chunk g/2
             // (or 4 + g/2) of the key's row, XOR-swizzled by the key
-            const uint8_t* vb = v_stage<kKv>(ring, s);
+            const uint8_t* vb = v_stage<true>(ring, s);
             auto ldv = [&](int key, int hi) {
                 const int off = (((hi * 4 + (g >> 1)) ^ (key & 7)) << 4) + (g & 1) * 8;
                 return *reinterpret_cast<const uint2*>(vb + key * 128 + off);
@@ -435,7 +281,7 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
                 ptx::mma_16816_f16(acc.o[mt], a, pb0, pb1);
             }
         } else {
-            const uint32_t vb = ptx::smem_u32(v_stage<kKv>(ring, s));
+            const uint32_t vb = ptx::smem_u32(v_stage<false>(ring, s));
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
                 const int chunk = (mt & 3) * 2 + (mq & 1);
@@ -453,9 +299,8 @@ __device__ __forceinline__ bool consume_blocks(const Params& p, const uint32_t (
 
 // Consumer warp writes its partial (row max, row sum, O) to wp. Accumulator
 // tile mt holds dims mt * 16 + {g, g + 8} (bf16 path) or 8g + mt and
-// 64 + 8g + mt (E4M3 path). E2M1: stored at the bf16 path's places, which
-// are free of bank conflicts (place_of_dim finds them).
-template <int kKv>
+// 64 + 8g + mt (E4M3 path).
+template <bool kF8>
 __device__ __forceinline__ void store_warp_partial(const WarpAcc& acc, Partial& wp) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     float lsum[2];
@@ -475,19 +320,13 @@ __device__ __forceinline__ void store_warp_partial(const WarpAcc& acc, Partial& 
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
-        const int d0 = kKv == kKvE4m3 ? 8 * g + mt : mt * 16 + g;
-        const int d1 = kKv == kKvE4m3 ? 64 + 8 * g + mt : d0 + 8;
+        const int d0 = kF8 ? 8 * g + mt : mt * 16 + g;
+        const int d1 = kF8 ? 64 + 8 * g + mt : d0 + 8;
         wp.o[2 * t4][d0] = acc.o[mt][0];
         wp.o[2 * t4 + 1][d0] = acc.o[mt][1];
         wp.o[2 * t4][d1] = acc.o[mt][2];
         wp.o[2 * t4 + 1][d1] = acc.o[mt][3];
     }
-}
-
-// Where an E2M1 partial holds output dim d = 64a + 32y + 4g + e: row g + 8y of
-// MMA tile 4a + e.
-__device__ __forceinline__ int place_of_dim(int d) {
-    return ((d >> 6) * 4 + (d & 3)) * 16 + ((d >> 5) & 1) * 8 + ((d >> 2) & 7);
 }
 
 // The heads a CTA finalises: CTA r of a cluster of CL owns heads r, r + CL,
@@ -557,7 +396,6 @@ __device__ __forceinline__ void merge_owned_and_store(const Params& p, int CL, i
     const int nh = (p.gq - r + CL - 1) / CL;  // heads r, r + CL, ... below gq
     for (int x = threadIdx.x; x < nh * kD; x += blockDim.x) {
         const int k = x / kD, d = x % kD, n = r + k * CL;
-        const int at = p.kv_f4 ? place_of_dim(d) : d;
         float M = -INFINITY;
         for (int c = 0; c < CL; ++c) M = fmaxf(M, owned.m[c * per + k]);
         float num = 0.f, den = 0.f;
@@ -565,38 +403,32 @@ __device__ __forceinline__ void merge_owned_and_store(const Params& p, int CL, i
             for (int c = 0; c < CL; ++c) {
                 const float mc = owned.m[c * per + k];
                 const float wgt = mc == -INFINITY ? 0.f : ptx::ex2_approx(mc - M);
-                num = fmaf(wgt, owned.o[c * per + k][at], num);
+                num = fmaf(wgt, owned.o[c * per + k][d], num);
                 den = fmaf(wgt, owned.l[c * per + k], den);
             }
         }
         float o = den > 0.f ? num / den : 0.f;
-        if (p.kv_f4 && isnan(den)) o = den;  // a NaN key's or value's rows
-        if (p.kv_f8 || p.kv_f4) o *= p.v_scale;
+        if (p.kv_f8) o *= p.v_scale;
         out[((int64_t)b * p.q_len * p.Hq + (int64_t)h * p.gq + n) * kD + d] =
             __float2bfloat16_rn(o);
     }
 }
 
-// Issue the loads of one 16-row block into ring stage s: TMA tiles of K and V
-// (two 64-column bf16 halves each, or one 128-byte-wide E4M3 panel each), or
-// a bulk copy of one page each. row: the block's first row in the source.
-template <int kKv>
+// Issue the TMA loads of one 16-row block into ring stage s: K and V, two
+// 64-column bf16 halves each, or one 128-byte-wide E4M3 panel each.
+template <bool kF8>
 __device__ __forceinline__ void issue_block(Ring& ring, uint64_t* full, int s,
-                                            const Source<kKv>& src, int row, int64_t outer) {
-    ptx::mbar_arrive_expect_tx(&full[s], 2 * blk_bytes<kKv>());
-    if constexpr (kKv == kKvE2m1) {
-        const int64_t at = outer * src.slab + (int64_t)(row / kGroupRows) * kE2m1Page;
-        ptx::bulk_g2s(k_stage<kKv>(ring, s), src.k + at, kE2m1Page, &full[s]);
-        ptx::bulk_g2s(v_stage<kKv>(ring, s), src.v + at, kE2m1Page, &full[s]);
-    } else if constexpr (kKv == kKvE4m3) {
-        ptx::tma_load_3d(k_stage<kKv>(ring, s), &src.k, 0, row, (int)outer, &full[s]);
-        ptx::tma_load_3d(v_stage<kKv>(ring, s), &src.v, 0, row, (int)outer, &full[s]);
+                                            const CUtensorMap* mk, const CUtensorMap* mv, int row,
+                                            int outer) {
+    if constexpr (kF8) {
+        ptx::mbar_arrive_expect_tx(&full[s], 2 * kBlkBytesF8);
+        ptx::tma_load_3d(k_stage<true>(ring, s), mk, 0, row, outer, &full[s]);
+        ptx::tma_load_3d(v_stage<true>(ring, s), mv, 0, row, outer, &full[s]);
     } else {
+        ptx::mbar_arrive_expect_tx(&full[s], 2 * kBlkBytes);
         for (int hf = 0; hf < 2; ++hf) {
-            ptx::tma_load_3d(k_stage<kKv>(ring, s) + hf * 2048, &src.k, hf * 64, row, (int)outer,
-                             &full[s]);
-            ptx::tma_load_3d(v_stage<kKv>(ring, s) + hf * 2048, &src.v, hf * 64, row, (int)outer,
-                             &full[s]);
+            ptx::tma_load_3d(k_stage<false>(ring, s) + hf * 2048, mk, hf * 64, row, outer, &full[s]);
+            ptx::tma_load_3d(v_stage<false>(ring, s) + hf * 2048, mv, hf * 64, row, outer, &full[s]);
         }
     }
 }
@@ -607,9 +439,9 @@ __device__ __forceinline__ void issue_block(Ring& ring, uint64_t* full, int s,
 // is armed again only after its previous phase completed, so the last armed
 // phase of each stage covers all of that stage's copies. False if a copy did
 // not land within the drain limit.
-template <int kKv>
+template <bool kF8>
 __device__ __forceinline__ bool drain_ring(uint64_t* full, int n_issued) {
-    constexpr int S = ring_stages<kKv>();
+    constexpr int S = ring_stages<kF8>();
     bool ok = true;
     for (int s = 0; s < S && s < n_issued; ++s) {
         const int last = s + ((n_issued - 1 - s) / S) * S;

@@ -2,9 +2,8 @@
 //
 // A page holds the rows of 16 tokens of one tensor (d = 128): the codes as
 // four tiles of 32 dims, each 16 rows x 16 bytes, then 16 rows x 8 E4M3
-// scales (one per 16 dims). Tiles, not whole rows: eight rows' 16-byte pieces
-// of a tile are 128 contiguous bytes, so the 8x8 matrix loads of decode
-// attention (ldmatrix) touch every shared-memory bank once.
+// scales (one per 16 dims). Tiles, not whole rows: 16-byte pieces of a row
+// that a kernel can place freely in shared memory.
 #pragma once
 
 #include "hga_common.cuh"
@@ -78,7 +77,7 @@ __device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t c, int half)
 }
 
 // The low half of every byte of a, and the high half of every byte of b.
-__device__ __forceinline__ uint32_t select_low_nibbles(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t select_nibbles(uint32_t a, uint32_t b) {
     return (a & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
 }
 

@@ -109,16 +109,21 @@ cudaError_t launch_attend_tc(const Params& p, const void* q_rot, const KvSources
                              const int32_t* sel_groups, const int32_t* n_sel_groups, void* out,
                              cudaStream_t st);
 
-// True when the cluster / MMA decode kernel covers this configuration
-// (bf16, d = 128, one query token, gq <= 8, L % 16 == 0, <= 128 key blocks).
+// True when the cluster / MMA decode kernels cover this configuration (bf16,
+// d = 128, one query token, gq <= 8, and L % 16 == 0 or the 4-bit store).
 bool decode_kernel_supports(const Params& p);
 
 cudaError_t launch_attend_decode(const Params& p, const void* q_rot, const KvSources& kv,
                                  const int32_t* sel_groups, const int32_t* n_sel_groups,
                                  void* out, cudaStream_t st);
 
+// Its form over a 4-bit store, which launch_attend_decode calls.
+cudaError_t launch_attend_pages(const Params& p, const void* q_rot, const KvSources& kv,
+                                const int32_t* sel_groups, const int32_t* n_sel_groups, void* out,
+                                cudaStream_t st);
+
 // One-launch decode step (q-bar, both routing levels, attention): bf16,
-// d = 128, one query token, gq <= 8, L % 16 == 0, top_k_chunks <= 64,
+// d = 128, one query token, gq <= 8, L % 16 == 0 (any L of a 4-bit store), top_k_chunks <= 64,
 // top_k_groups <= 512, and routing tables that fit one cluster's shared
 // memory. With out == nullptr it stops after routing. The keys come from
 // k_cache / v_cache in p.kv_layout: the full resident store, or (with

@@ -10,14 +10,14 @@
 // One cluster of CL CTAs per (sequence, KV head), CL chosen so the grid
 // fills every SM with two CTAs at once. CTA r owns a contiguous share of the
 // unit's 16-row key blocks and streams them through a shared-memory ring
-// (8 stages, 16 of E4M3 blocks or 24 of E2M1 pages) filled by TMA (tensor-map
-// tile loads, 128-byte swizzle, or bulk copies of pages; one producer thread). Eight consumer warps take every 8th block: S^T[16 keys x 8 heads]
+// (8 stages, or 16 of E4M3 blocks) filled by TMA (tensor-map tile loads,
+// 128-byte swizzle; one producer thread). Eight consumer warps take every 8th block: S^T[16 keys x 8 heads]
 // = K_blk Q^T and O^T[128 dims x 8 heads] += V^T P^T on warp-level bf16 MMA
 // (m16n8k16, fp32 accumulate) with a per-warp online softmax in fp32. The
 // 8 x CL warp partials (max, sum, O) merge through distributed shared memory:
 // CTA r finalises heads r, r + CL, ... With E4M3 keys and values
-// (HGA_KV_E4M3) the blocks are 2 KiB per tensor, with E2M1 ones 1152 bytes,
-// and the products run on fp16 MMA (hga_decode_core.cuh).
+// (HGA_KV_E4M3) the blocks are 2 KiB per tensor and the products run on fp16
+// MMA (hga_decode_core.cuh).
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -41,9 +41,8 @@ using dec::kMaxCluster;
 using dec::kStagesMax;
 using dec::kThreads;
 
-template <int kKv>
-struct DecodeSources {
-    dec::Source<kKv> res, gat;
+struct DecodeMaps {
+    CUtensorMap k_res, v_res, k_gat, v_gat;
 };
 
 struct DecodeSmem {
@@ -61,9 +60,9 @@ struct DecodeSmem {
     int bad;
 };
 
-template <int kKv>
+template <bool kF8>
 __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
-    const __grid_constant__ DecodeSources<kKv> src, Params p, const __nv_bfloat16* __restrict__ q,
+    const __grid_constant__ DecodeMaps maps, Params p, const __nv_bfloat16* __restrict__ q,
     const int32_t* __restrict__ sel, const int32_t* __restrict__ nsel,
     __nv_bfloat16* __restrict__ out, int gathered) {
     extern __shared__ uint8_t smem_raw[];
@@ -104,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
         if (lane == 0) {
             int i = 0;
             for (; i < nloc; ++i) {
-                constexpr int kS = dec::ring_stages<kKv>();
+                constexpr int kS = dec::ring_stages<kF8>();
                 const int s = i % kS;
                 if (i >= kS &&
                     !ptx::mbar_wait_bounded(&sm.empty[s], ((i / kS) - 1) & 1, p.wait_ns)) {
@@ -115,11 +114,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
                 const int rw = sm.blk_row[lo + i];
                 const bool gat = (rw & kSrcGathered) != 0;
                 const int row = rw & ~kSrcGathered;
-                dec::issue_block<kKv>(sm.u.ring, sm.full, s, gat ? src.gat : src.res, row,
-                                      gat ? prob : kvh);
+                dec::issue_block<kF8>(sm.u.ring, sm.full, s, gat ? &maps.k_gat : &maps.k_res,
+                                 gat ? &maps.v_gat : &maps.v_res, row, (int)(gat ? prob : kvh));
             }
             // every issued load lands before the ring's memory is reused
-            if (!dec::drain_ring<kKv>(sm.full, i)) {
+            if (!dec::drain_ring<kF8>(sm.full, i)) {
                 raise_timeout(p);
                 sm.bad = 1;
             }
@@ -131,15 +130,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
     dec::acc_init(acc);
     if (warp < kConsumers) {
         uint32_t qf[8][2];
-        float sc[2];
-        dec::load_q_frags<kKv>(p, q, b, h, qf, sc);
-        dec::consume_blocks<kKv>(p, qf, sc, sm.u.ring, sm.full, sm.empty, sm.blk_pos + lo, nloc,
+        dec::load_q_frags<kF8>(p, q, b, h, qf);
+        dec::consume_blocks<kF8>(p, qf, sm.u.ring, sm.full, sm.empty, sm.blk_pos + lo, nloc,
                             p.q_begin, sm.pt[warp], acc, &sm.bad);
     }
     __syncthreads();  // ring drained: every stage a consumer used was waited for
 
     // ---- per-warp partials -> shared memory (the ring's space is reused)
-    if (warp < kConsumers) dec::store_warp_partial<kKv>(acc, sm.u.warp_part[warp]);
+    if (warp < kConsumers) dec::store_warp_partial<kF8>(acc, sm.u.warp_part[warp]);
     __syncthreads();
     dec::merge_warps_push(sm.u.warp_part, cluster, sm.owned, sm.wgt, p.gq);
     cluster.sync();  // every partial is in its owner's shared memory
@@ -150,12 +148,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
 std::mutex g_decode_mu;
 // per device and K/V type: clusters of each size resident at once (0 = not
 // queried) and the largest cluster size that co-schedules
-int g_dec_active[kMaxDevicesPerProcess][3][kMaxCluster + 1] = {};
-int g_dec_max_cluster[kMaxDevicesPerProcess][3] = {};
+int g_dec_active[kMaxDevicesPerProcess][2][kMaxCluster + 1] = {};
+int g_dec_max_cluster[kMaxDevicesPerProcess][2] = {};
 
 // Cluster size: as many CTAs per (sequence, KV head) as keep every unit's
 // cluster resident at once (one wave), per the occupancy query for clusters.
-template <int kKv>
+template <bool kF8>
 int pick_cluster(const Params& p, size_t smem, int dev) {
     int sms = 148;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -163,7 +161,7 @@ int pick_cluster(const Params& p, size_t smem, int dev) {
     int cl = 2 * sms / units;  // two CTAs per SM
     cl = cl < 1 ? 1 : (cl > kMaxCluster ? kMaxCluster : cl);
     std::lock_guard<std::mutex> lock(g_decode_mu);
-    int* max_active = g_dec_active[dev][kKv];
+    int* max_active = g_dec_active[dev][kF8 ? 1 : 0];
     for (; cl > 1; --cl) {
         if (max_active[cl] == 0) {
             cudaLaunchConfig_t q = {};
@@ -178,7 +176,7 @@ int pick_cluster(const Params& p, size_t smem, int dev) {
             q.attrs = a;
             q.numAttrs = 1;
             int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, attend_decode_kernel<kKv>, &q) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&n, attend_decode_kernel<kF8>, &q) != cudaSuccess) {
                 cudaGetLastError();
                 n = -1;
             }
@@ -193,60 +191,51 @@ int pick_cluster(const Params& p, size_t smem, int dev) {
 
 namespace {
 
-template <int kKv>
+template <bool kF8>
 cudaError_t launch_decode_t(const Params& p, const void* q_rot, const KvSources& kv,
                             const int32_t* sel_groups, const int32_t* n_sel_groups, void* out,
                             cudaStream_t st) {
-    DecodeSources<kKv> src;
+    DecodeMaps maps;
     const bool gathered = kv.k_gat != nullptr;
     const int64_t res_rows = p.kv_layout == HGA_KV_WINDOWS
                                  ? (int64_t)(p.n_sink + p.n_local + 1) * p.C
                                  : (int64_t)p.L;
     const int64_t BH = (int64_t)p.B * p.Hkv;
-    if constexpr (kKv == dec::kKvE2m1) {
-        auto pages = [](const void* k, const void* v, int64_t rows) {
-            return dec::PageSource{(const uint8_t*)k, (const uint8_t*)v,
-                                   (rows + kGroupRows - 1) / kGroupRows * kE2m1Page};
-        };
-        src.res = pages(kv.k_res, kv.v_res, res_rows);
-        src.gat = gathered ? pages(kv.k_gat, kv.v_gat, (int64_t)p.kg * kGroupRows) : src.res;
+    auto rows_map = [](CUtensorMap* m, const void* base, int64_t outer, int64_t rows) {
+        return kF8 ? make_rows_map_u8(m, base, outer, rows, kD, kGroupRows)
+                   : make_rows_map(m, base, outer, rows, kD, kGroupRows);
+    };
+    bool ok = rows_map(&maps.k_res, kv.k_res, BH, res_rows) &&
+              rows_map(&maps.v_res, kv.v_res, BH, res_rows);
+    if (gathered) {
+        ok = ok && rows_map(&maps.k_gat, kv.k_gat, BH * p.nQC, (int64_t)p.kg * kGroupRows) &&
+             rows_map(&maps.v_gat, kv.v_gat, BH * p.nQC, (int64_t)p.kg * kGroupRows);
     } else {
-        auto rows_map = [](CUtensorMap* m, const void* base, int64_t outer, int64_t rows) {
-            return kKv == dec::kKvE4m3 ? make_rows_map_u8(m, base, outer, rows, kD, kGroupRows)
-                                       : make_rows_map(m, base, outer, rows, kD, kGroupRows);
-        };
-        bool ok = rows_map(&src.res.k, kv.k_res, BH, res_rows) &&
-                  rows_map(&src.res.v, kv.v_res, BH, res_rows);
-        if (gathered) {
-            const int64_t rows = (int64_t)p.kg * kGroupRows;
-            ok = ok && rows_map(&src.gat.k, kv.k_gat, BH * p.nQC, rows) &&
-                 rows_map(&src.gat.v, kv.v_gat, BH * p.nQC, rows);
-        } else {
-            src.gat = src.res;
-        }
-        if (!ok) return cudaErrorInvalidValue;
+        maps.k_gat = maps.k_res;
+        maps.v_gat = maps.v_res;
     }
+    if (!ok) return cudaErrorInvalidValue;
     const size_t smem = sizeof(DecodeSmem) + 1024;
     int dev = 0;
     cudaError_t e = current_device_index(&dev);
     if (e != cudaSuccess) return e;
-    e = set_func_attr_once((const void*)attend_decode_kernel<kKv>,
+    e = set_func_attr_once((const void*)attend_decode_kernel<kF8>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-        e = set_func_attr_once((const void*)attend_decode_kernel<kKv>,
+        e = set_func_attr_once((const void*)attend_decode_kernel<kF8>,
                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     int max_cluster = 0;
     {
         std::lock_guard<std::mutex> lock(g_decode_mu);
-        int& mc_slot = g_dec_max_cluster[dev][kKv];
+        int& mc_slot = g_dec_max_cluster[dev][kF8 ? 1 : 0];
         if (mc_slot <= 0) {
             cudaLaunchConfig_t q = {};
             q.gridDim = dim3(kMaxCluster, 1, 1);
             q.blockDim = dim3(kThreads);
             q.dynamicSmemBytes = smem;
             int mc = 0;
-            if (cudaOccupancyMaxPotentialClusterSize(&mc, attend_decode_kernel<kKv>, &q) !=
+            if (cudaOccupancyMaxPotentialClusterSize(&mc, attend_decode_kernel<kF8>, &q) !=
                 cudaSuccess) {
                 cudaGetLastError();
                 return cudaErrorInvalidConfiguration;
@@ -255,7 +244,7 @@ cudaError_t launch_decode_t(const Params& p, const void* q_rot, const KvSources&
         }
         max_cluster = mc_slot;
     }
-    int cl = pick_cluster<kKv>(p, smem, dev);
+    int cl = pick_cluster<kF8>(p, smem, dev);
     if (cl > max_cluster) cl = max_cluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cl, (unsigned)((int64_t)p.B * p.Hu), 1);
@@ -270,7 +259,7 @@ cudaError_t launch_decode_t(const Params& p, const void* q_rot, const KvSources&
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int gflag = gathered ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<kKv>, src, p,
+    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<kF8>, maps, p,
                               (const __nv_bfloat16*)q_rot, sel_groups, n_sel_groups,
                               (__nv_bfloat16*)out, gflag);
 }
@@ -280,11 +269,10 @@ cudaError_t launch_decode_t(const Params& p, const void* q_rot, const KvSources&
 cudaError_t launch_attend_decode(const Params& p, const void* q_rot, const KvSources& kv,
                                  const int32_t* sel_groups, const int32_t* n_sel_groups,
                                  void* out, cudaStream_t st) {
-    if (p.kv_f4)
-        return launch_decode_t<dec::kKvE2m1>(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
+    if (p.kv_f4) return launch_attend_pages(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
     if (p.kv_f8)
-        return launch_decode_t<dec::kKvE4m3>(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
-    return launch_decode_t<dec::kKvBf16>(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
+        return launch_decode_t<true>(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
+    return launch_decode_t<false>(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
 }
 
 bool decode_kernel_supports(const Params& p) {

@@ -30,12 +30,16 @@
 // exact and unique. The scores are the same fp32 dot products, summed in the
 // same order, as the separate routing kernels, so both paths select the same
 // sets. Attention then runs as in the split-K decode kernel on CTA r's share
-// of the forced blocks and of the routed blocks (hga_decode_core.cuh).
+// of the forced blocks and of the routed blocks (hga_decode_core.cuh). A 4-bit
+// store's pages go the way of hga_decode_pages.cuh: every consumer warp copies
+// its own, from the device or from the host store, and the forced ones are
+// only fetched into L2 ahead of the routing.
 #include <cooperative_groups.h>
 
 #include <mutex>
 
 #include "hga_decode_core.cuh"
+#include "hga_decode_pages.cuh"
 #include "hga_kernels.h"
 #include "hga_tmap.h"
 #include "hga_topk.cuh"
@@ -61,7 +65,16 @@ constexpr int kMaxLocal = 256;   // key blocks per CTA
 constexpr int kRankThreads = kConsumers * 32;
 constexpr int kL1Rows = 16;      // level-1 rows per consumer warp per batch
 
-struct StepSmem {
+// How keys and values are stored.
+constexpr int kKvBf16 = 0, kKvE4m3 = 1, kKvE2m1 = 2;
+
+struct StepMaps {
+    CUtensorMap k, v;
+};
+template <int kKv>
+using StepSource = std::conditional_t<kKv == kKvE2m1, dec::PageSource, StepMaps>;
+
+struct StepRing {
     union {
         dec::Ring ring;
         dec::Partial warp_part[kConsumers];
@@ -70,6 +83,9 @@ struct StepSmem {
     float wgt[kConsumers][8];                    // warp-merge weights
     uint16_t pt[kConsumers][8][16];
     uint64_t full[kStagesMax], empty[kStagesMax];
+};
+
+struct StepTables {
     alignas(16) uint64_t key1[kMaxSlice];     // own level-1 candidates
     uint64_t own1[kMaxKc];        // this CTA's level-1 finalists, ascending
     alignas(16) uint64_t f1[kMaxF1];          // level-1 finalists of all CTAs
@@ -78,9 +94,12 @@ struct StepSmem {
     int win1[kMaxKc];             // selected chunks, ascending
     int routed[kMaxKg];           // selected groups, ascending
     int blk_pos[kMaxLocal];       // position of a local block's first key
-    int blk_row[kMaxLocal];       // its first row in the resident store (TMA source)
+    int blk_row[kMaxLocal];       // its first row in its store
     int n_win1, n_wl, bad;
 };
+
+template <int kKv>
+struct StepSmem : std::conditional_t<kKv == kKvE2m1, dec::PageSmem, StepRing>, StepTables {};
 
 __device__ __forceinline__ uint64_t rank_key(uint32_t key32, int idx) {
     return key32 ? ((uint64_t)key32 << 32) | (uint32_t)(0x7fffffff - idx) : 0ull;
@@ -186,33 +205,26 @@ __device__ __forceinline__ void score_rows(const float* q, int n, RowOf row_of, 
 // link with 16-byte loads (each lane 8 (bf16) or 4 (E4M3) of each tensor,
 // 512 contiguous bytes per warp load) and stored into ring stage s in the
 // layout the TMA tile loads write: 128-byte panels of 16 rows (two for bf16,
-// one for E4M3), 16-byte chunk c of row r at c ^ (r % 8). An E2M1 group is
-// one page of 72 pieces and is copied as it is.
-template <int kKv>
+// one for E4M3), 16-byte chunk c of row r at c ^ (r % 8).
+template <bool kF8>
 __device__ __forceinline__ void copy_host_block(dec::Ring& ring, int s, const uint4* kh,
                                                 const uint4* vh) {
     const int lane = threadIdx.x & 31;
-    constexpr int kVecs = dec::blk_bytes<kKv>() / 16;
-    constexpr int kPieces = (kVecs + 31) / 32;       // per lane per tensor
-    constexpr int kRowPieces = kKv == dec::kKvE4m3 ? 8 : 16;  // 16-byte pieces per row
+    constexpr int kPieces = kF8 ? 4 : 8;             // per lane per tensor
+    constexpr int kRowPieces = kF8 ? 8 : 16;         // 16-byte pieces per row
     uint4 kr[kPieces], vr[kPieces];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-        if (kVecs % 32 == 0 || lane + 32 * u < kVecs) {
-            kr[u] = kh[lane + 32 * u];
-            vr[u] = vh[lane + 32 * u];
-        }
+        kr[u] = kh[lane + 32 * u];
+        vr[u] = vh[lane + 32 * u];
     }
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
         const int idx = lane + 32 * u;               // 16-byte piece of the block
-        if (kVecs % 32 != 0 && idx >= kVecs) break;
         const int row = idx / kRowPieces, c16 = idx % kRowPieces;
-        const int off = kKv == dec::kKvE2m1
-                            ? idx * 16
-                            : (c16 >> 3) * 2048 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(dec::k_stage<kKv>(ring, s) + off) = kr[u];
-        *reinterpret_cast<uint4*>(dec::v_stage<kKv>(ring, s) + off) = vr[u];
+        const int off = (c16 >> 3) * 2048 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(dec::k_stage<kF8>(ring, s) + off) = kr[u];
+        *reinterpret_cast<uint4*>(dec::v_stage<kF8>(ring, s) + off) = vr[u];
     }
     // a later tile load into this stage (async proxy) is ordered after these
     // stores
@@ -220,21 +232,22 @@ __device__ __forceinline__ void copy_host_block(dec::Ring& ring, int s, const ui
 }
 
 // S: element type of the summary tables (float, or bf16 for bf16 tables).
-// kKv: how keys and values are stored (hga_decode_core.cuh).
+// kKv: how keys and values are stored.
 // k_host / v_host: nullptr, or the full store [B, Hkv, L, d] in mapped host
 // memory (the host tier); then src covers the resident windows of the
 // forced chunks ([B, Hkv, W * C, d]) and the routed groups are read from the
 // host by the producer warp.
 template <typename S, int kKv>
 __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
-    const __grid_constant__ dec::Source<kKv> src, Params p, const __nv_bfloat16* __restrict__ q,
+    const __grid_constant__ StepSource<kKv> src, Params p, const __nv_bfloat16* __restrict__ q,
     const S* __restrict__ cs, const S* __restrict__ gs, float* __restrict__ qbar_out,
     int32_t* __restrict__ sel_c, int32_t* __restrict__ nsel_c, int32_t* __restrict__ sel_g,
     int32_t* __restrict__ nsel_g, __nv_bfloat16* __restrict__ out, int attend,
     const uint4* __restrict__ k_host, const uint4* __restrict__ v_host) {
     extern __shared__ uint8_t smem_raw[];
-    StepSmem& sm = *reinterpret_cast<StepSmem*>(
-        align_smem_1024(smem_raw));
+    using Smem = StepSmem<kKv>;
+    Smem& sm = *reinterpret_cast<Smem*>(align_smem_1024(smem_raw));
+    constexpr bool kF8 = kKv == kKvE4m3, kPages = kKv == kKvE2m1;
     cg::cluster_group cluster = cg::this_cluster();
     const int CL = (int)cluster.num_blocks();
     const int r = (int)cluster.block_rank();
@@ -260,11 +273,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
         sm.bad = 0;
         sm.n_win1 = 0;
         sm.n_wl = 0;
-        for (int s = 0; s < kStagesMax; ++s) {
-            ptx::mbar_init(&sm.full[s], 1);
-            ptx::mbar_init(&sm.empty[s], 1);
+        if constexpr (!kPages) {
+            for (int s = 0; s < kStagesMax; ++s) {
+                ptx::mbar_init(&sm.full[s], 1);
+                ptx::mbar_init(&sm.empty[s], 1);
+            }
+            ptx::fence_mbar_init();
         }
-        ptx::fence_mbar_init();
     }
     const bool host_tier = k_host != nullptr;
     for (int i = tid; i < nf_loc; i += blockDim.x) {
@@ -275,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
         sm.blk_row[i] = host_tier ? w * p.C + kGroupRows * gm : sm.blk_pos[i];
     }
     __syncthreads();
-    constexpr int kS = dec::ring_stages<kKv>();
+    constexpr int kS = dec::ring_stages<kF8>();
     const int n_pre = nf_loc < kS ? nf_loc : kS;
 
     // ---- level-1 slice: the first batch of this warp's chunk-summary rows is
@@ -360,9 +375,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
     // the forced blocks' loads are issued once the level-1 rows are in: they
     // are needed only after routing, and the chunk-summary reads above are
     // on the critical path
-    if (attend && warp == kConsumers && lane == 0)
+    if constexpr (kPages) {
+        if (attend && warp == kConsumers)
+            for (int i = lane; i < nf_loc; i += 32) {
+                const int64_t at = kvh * src.slab + (int64_t)(sm.blk_row[i] / kGroupRows) * kE2m1Page;
+                ptx::bulk_prefetch_l2(src.k + at, kE2m1Page);
+                ptx::bulk_prefetch_l2(src.v + at, kE2m1Page);
+            }
+    } else if (attend && warp == kConsumers && lane == 0) {
         for (int i = 0; i < n_pre; ++i)
-            dec::issue_block<kKv>(sm.u.ring, sm.full, i, src, sm.blk_row[i], kvh);
+            dec::issue_block<kF8>(sm.u.ring, sm.full, i, &src.k, &src.v, sm.blk_row[i], (int)kvh);
+    }
     // this CTA's winners, in candidate (= ascending chunk) order, padded
     // with 0 to cap1 entries. (Prefetching the winners' group rows into L2
     // here, with one bulk prefetch per winner, cost more in this phase than
@@ -439,63 +462,84 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
     }
     const int nloc = nf_loc + nr_loc;
     __syncthreads();
-    if (warp == kConsumers) {
-        // lane 0 waits for free stages and issues the tile loads of resident
-        // blocks; a routed block of the host tier is copied by the whole warp
-        // (its stage's barrier then completes on lane 0's plain arrival)
-        int i = n_pre;
-        bool ok = true;
-        for (; i < nloc; ++i) {
-            const int s = i % kS;
-            if (i >= kS) {
-                bool got = true;
-                if (lane == 0)
-                    got = ptx::mbar_wait_bounded(&sm.empty[s], ((i / kS) - 1) & 1, p.wait_ns);
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
-                    ok = false;
-                    break;
+    if constexpr (kPages) {
+        dec::WarpAcc acc;
+        dec::acc_init(acc);
+        if (consumer) {
+            uint32_t qf[8][2];
+            float sc[2];
+            dec::load_q_pages(p, q, b, h, qf, sc);
+            dec::consume_pages(
+                qf, sc, sm.u.page[warp], (nloc - warp + kConsumers - 1) / kConsumers, p.q_begin,
+                [&](int i) {
+                    const int x = warp + kConsumers * i;
+                    const bool host = host_tier && x >= nf_loc;
+                    const int64_t at = kvh * (host ? p.kv_slab : src.slab) +
+                                       (int64_t)(sm.blk_row[x] / kGroupRows) * kE2m1Page;
+                    return dec::PageRef{(host ? (const uint8_t*)k_host : src.k) + at,
+                                        (host ? (const uint8_t*)v_host : src.v) + at,
+                                        sm.blk_pos[x]};
+                },
+                acc);
+        }
+        dec::merge_pages(sm, cluster, p, acc, b, h, out);
+    } else {
+        if (warp == kConsumers) {
+            // lane 0 waits for free stages and issues the tile loads of resident
+            // blocks; a routed block of the host tier is copied by the whole warp
+            // (its stage's barrier then completes on lane 0's plain arrival)
+            int i = n_pre;
+            bool ok = true;
+            for (; i < nloc; ++i) {
+                const int s = i % kS;
+                if (i >= kS) {
+                    bool got = true;
+                    if (lane == 0)
+                        got = ptx::mbar_wait_bounded(&sm.empty[s], ((i / kS) - 1) & 1, p.wait_ns);
+                    if (!__shfl_sync(0xffffffffu, got, 0)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (host_tier && i >= nf_loc) {
+                    const int64_t row = kvh * (int64_t)p.L + sm.blk_row[i];
+                    constexpr int kRowVecs = kF8 ? kD / 16 : kD / 8;  // 16-byte pieces per row
+                    copy_host_block<kF8>(sm.u.ring, s, k_host + row * kRowVecs, v_host + row * kRowVecs);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sm.full[s]);
+                } else if (lane == 0) {
+                    dec::issue_block<kF8>(sm.u.ring, sm.full, s, &src.k, &src.v, sm.blk_row[i], (int)kvh);
                 }
             }
-            if (host_tier && i >= nf_loc) {
-                // blocks of 16 rows lie one after another in a unit's slab
-                const int64_t at = kvh * (p.kv_slab / 16) +
-                                   (int64_t)(sm.blk_row[i] / kGroupRows) * (dec::blk_bytes<kKv>() / 16);
-                copy_host_block<kKv>(sm.u.ring, s, k_host + at, v_host + at);
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&sm.full[s]);
-            } else if (lane == 0) {
-                dec::issue_block<kKv>(sm.u.ring, sm.full, s, src, sm.blk_row[i], kvh);
+            if (lane == 0) {
+                if (!ok) {
+                    raise_timeout(p);
+                    sm.bad = 1;
+                }
+                // every issued load (the early forced blocks included) lands
+                // before the ring's memory is reused
+                if (!dec::drain_ring<kF8>(sm.full, i)) {
+                    raise_timeout(p);
+                    sm.bad = 1;
+                }
             }
         }
-        if (lane == 0) {
-            if (!ok) {
-                raise_timeout(p);
-                sm.bad = 1;
-            }
-            // every issued load (the early forced blocks included) lands
-            // before the ring's memory is reused
-            if (!dec::drain_ring<kKv>(sm.full, i)) {
-                raise_timeout(p);
-                sm.bad = 1;
-            }
+        dec::WarpAcc acc;
+        dec::acc_init(acc);
+        if (consumer) {
+            uint32_t qf[8][2];
+            dec::load_q_frags<kF8>(p, q, b, h, qf);
+            dec::consume_blocks<kF8>(p, qf, sm.u.ring, sm.full, sm.empty, sm.blk_pos, nloc, p.q_begin,
+                                sm.pt[warp], acc, &sm.bad);
         }
+        __syncthreads();
+        if (consumer) dec::store_warp_partial<kF8>(acc, sm.u.warp_part[warp]);
+        __syncthreads();
+        dec::merge_warps_push(sm.u.warp_part, cluster, sm.owned, sm.wgt, p.gq);
+        cluster.sync();  // every partial is in its owner's shared memory
+        dec::merge_owned_and_store(p, (int)cluster.num_blocks(), (int)cluster.block_rank(), sm.owned, b,
+                                   h, out);
     }
-    dec::WarpAcc acc;
-    dec::acc_init(acc);
-    if (consumer) {
-        uint32_t qf[8][2];
-        float sc[2];
-        dec::load_q_frags<kKv>(p, q, b, h, qf, sc);
-        dec::consume_blocks<kKv>(p, qf, sc, sm.u.ring, sm.full, sm.empty, sm.blk_pos, nloc, p.q_begin,
-                            sm.pt[warp], acc, &sm.bad);
-    }
-    __syncthreads();
-    if (consumer) dec::store_warp_partial<kKv>(acc, sm.u.warp_part[warp]);
-    __syncthreads();
-    dec::merge_warps_push(sm.u.warp_part, cluster, sm.owned, sm.wgt, p.gq);
-    cluster.sync();  // every partial is in its owner's shared memory
-    dec::merge_owned_and_store(p, (int)cluster.num_blocks(), (int)cluster.block_rank(), sm.owned, b,
-                               h, out);
 }
 
 // Table sizes a cluster of cl CTAs needs; false if one is over its cap.
@@ -592,7 +636,7 @@ cudaError_t launch_step(const Params& p, const void* q_rot, const S* chunk_sum,
                         int32_t* n_sel_groups, void* out, const void* k_host, const void* v_host,
                         cudaStream_t st) {
     const bool attend = out != nullptr;
-    dec::Source<kKv> src;
+    StepSource<kKv> src;
     memset(&src, 0, sizeof(src));
     if (attend) {
         const int64_t BH = (int64_t)p.B * p.Hkv;
@@ -600,10 +644,9 @@ cudaError_t launch_step(const Params& p, const void* q_rot, const S* chunk_sum,
                                  ? (int64_t)(p.n_sink + p.n_local + 1) * p.C
                                  : (int64_t)p.L;
         bool ok = true;
-        if constexpr (kKv == dec::kKvE2m1)
-            src = {(const uint8_t*)k_cache, (const uint8_t*)v_cache,
-                   (rows + kGroupRows - 1) / kGroupRows * kE2m1Page};
-        else if constexpr (kKv == dec::kKvE4m3)
+        if constexpr (kKv == kKvE2m1)
+            src = {(const uint8_t*)k_cache, (const uint8_t*)v_cache, dec::page_slab(rows)};
+        else if constexpr (kKv == kKvE4m3)
             ok = make_rows_map_u8(&src.k, k_cache, BH, rows, kD, kGroupRows) &&
                  make_rows_map_u8(&src.v, v_cache, BH, rows, kD, kGroupRows);
         else
@@ -611,7 +654,7 @@ cudaError_t launch_step(const Params& p, const void* q_rot, const S* chunk_sum,
                  make_rows_map(&src.v, v_cache, BH, rows, kD, kGroupRows);
         if (!ok) return cudaErrorInvalidValue;
     }
-    const size_t smem = sizeof(StepSmem) + 1024;
+    const size_t smem = sizeof(StepSmem<kKv>) + 1024;
     cudaError_t e = step_prepare<S, kKv>(smem);
     if (e != cudaSuccess) return e;
     const int cl = step_cluster<S, kKv>(p, smem);
@@ -649,9 +692,9 @@ cudaError_t launch_decode_step(const Params& p, const void* q_rot, const void* c
             n_sel_chunks, sel_groups, n_sel_groups, out, k_host, v_host, st);
     };
     auto by_kv = [&](auto s) {
-        if (p.kv_f4) return run(s, std::integral_constant<int, dec::kKvE2m1>());
-        if (p.kv_f8) return run(s, std::integral_constant<int, dec::kKvE4m3>());
-        return run(s, std::integral_constant<int, dec::kKvBf16>());
+        if (p.kv_f4) return run(s, std::integral_constant<int, kKvE2m1>());
+        if (p.kv_f8) return run(s, std::integral_constant<int, kKvE4m3>());
+        return run(s, std::integral_constant<int, kKvBf16>());
     };
     return p.sum_bf16 ? by_kv(bf()) : by_kv(float());
 }
