@@ -101,13 +101,19 @@ cudaError_t launch_attend_simt(const Params& p, const void* q_rot, const KvSourc
                                const int32_t* sel_groups, const int32_t* n_sel_groups,
                                void* out, cudaStream_t st);
 
-// True when the tcgen05 prefill kernel covers this configuration (bf16,
-// d = 128, 8 query heads per KV head, prefill, full resident store, index mode).
+// True when a tcgen05 prefill kernel covers this configuration (d = 128,
+// prefill, full resident store, index mode; bf16 with 8 query heads per KV
+// head, or the 4-bit store with up to 128).
 bool tc_kernel_supports(const Params& p, bool gathered);
 
 cudaError_t launch_attend_tc(const Params& p, const void* q_rot, const KvSources& kv,
                              const int32_t* sel_groups, const int32_t* n_sel_groups, void* out,
                              cudaStream_t st);
+
+// Its form over a 4-bit store, which launch_attend_tc calls.
+cudaError_t launch_attend_tc_pages(const Params& p, const void* q_rot, const KvSources& kv,
+                                   const int32_t* sel_groups, const int32_t* n_sel_groups,
+                                   void* out, cudaStream_t st);
 
 // True when the cluster / MMA decode kernels cover this configuration (bf16,
 // d = 128, one query token, gq <= 8, and L % 16 == 0 or the 4-bit store).

@@ -94,6 +94,12 @@ __device__ __forceinline__ void bulk_g2s(void* dst_smem, const void* src_gmem, u
         : "memory");
 }
 
+// This thread's shared-memory writes become visible to the async proxy (tensor
+// core and bulk-copy reads) that a later barrier arrival releases.
+__device__ __forceinline__ void fence_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // 16 bytes global -> shared, tracked by the issuing thread's copy groups.
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src_gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src_gmem)
@@ -264,6 +270,14 @@ __device__ __forceinline__ void add_bf16x2_f32(uint32_t packed, float& acc0, flo
         : "r"(packed));
 }
 
+// The same for two f16 halves.
+__device__ __forceinline__ void add_f16x2_f32(uint32_t packed, float& acc0, float& acc1) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
+        : "+f"(acc0), "+f"(acc1)
+        : "r"(packed));
+}
+
 // (d0, d1) = (a0, a1) * b + c with one packed fp32x2 FMA (sm_100); each lane
 // rounds once, exactly like two fmaf calls.
 __device__ __forceinline__ void fma2_bc(float a0, float a1, float b, float c, float& d0,
@@ -423,6 +437,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) |
            ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// The same with f16 A/B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+// This warpgroup's registers per thread (all four warps execute it).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 }  // namespace ptx

@@ -39,24 +39,19 @@
 #include "hga_blocks.cuh"
 #include "hga_kernels.h"
 #include "hga_ptx.cuh"
+#include "hga_tc.cuh"
 #include "hga_tmap.h"
 
 namespace hga {
 
 namespace {
 
-constexpr int kD = 128;
-constexpr int kRows = 128;                 // query rows per M tile
-constexpr int kTileKeys = 128;             // keys per tile
-constexpr int kBlocksPerTile = kTileKeys / kGroupRows;
-constexpr int kPanel = 128 * 128;          // 128 rows x 128 bytes (64 bf16)
-constexpr int kTile = 2 * kPanel;          // 128 x 128 bf16
-constexpr int kThreads = 352;  // 11 warps
-constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.0f;
+using namespace tc;
 
-__host__ __device__ constexpr uint32_t col_s(int x) { return (uint32_t)(x * 128); }
-__host__ __device__ constexpr uint32_t col_o(int x) { return (uint32_t)(256 + x * 128); }
+constexpr uint32_t kIdQk = ptx::idesc_bf16_f32(kRows, kTileKeys, 0, 0);
+constexpr uint32_t kIdPv = ptx::idesc_bf16_f32(kRows, kD, 0, 1);
+
+constexpr int kThreads = 352;  // 11 warps
 
 struct TcMaps {
     CUtensorMap q, k, v;
@@ -97,43 +92,6 @@ __device__ __forceinline__ bool unit_at(const Params& p, int u, Unit& un) {
     un.j = p.j0 + un.jj;
     un.tok0 = un.j * p.C + un.pair * 32;
     return un.tok0 < p.q_begin + p.q_len && un.tok0 + 32 > p.q_begin;
-}
-
-// Bounded wait shared by the roles of one CTA: gives up after the launch's
-// wait limit or when another role of this CTA gave up (*abort); a give-up
-// sets *abort so the other roles stop. Both are checked every 8 polls. The
-// device error word is not consulted: an invalid selection entry (of this
-// unit or any other, in this launch or an earlier one) never stops a wait.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         uint64_t limit_ns) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    for (uint32_t i = 0;; ++i) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((i & 7u) == 7u && (*abort || ptx::globaltimer_ns() - t0 > limit_ns)) break;
-    }
-    *abort = 1;
-    return false;
-}
-
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_s, uint32_t k_s) {
-    constexpr uint32_t id_qk = ptx::idesc_bf16_f32(kRows, kTileKeys, 0, 0);
-#pragma unroll
-    for (int kk = 0; kk < kD / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-        ptx::umma_f16(d_tmem, ptx::smem_desc_sw128(q_s + off, 16, 1024),
-                      ptx::smem_desc_sw128(k_s + off, 16, 1024), id_qk, kk > 0);
-    }
-}
-
-// O (+)= P V with P (bf16) in TMEM columns [p_tmem, p_tmem + 64).
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_s,
-                                         bool accumulate) {
-    constexpr uint32_t id_pv = ptx::idesc_bf16_f32(kRows, kD, 0, 1);
-#pragma unroll
-    for (int kk = 0; kk < kTileKeys / 16; ++kk)
-        ptx::umma_f16_ts(d_tmem, p_tmem + kk * 8,
-                         ptx::smem_desc_sw128(v_s + kk * 2048, kPanel, 1024), id_pv,
-                         (accumulate || kk > 0) ? 1u : 0u);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ TcMaps maps,
@@ -299,9 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 // S_x of the previous unit was read and its P consumed by the PV
                 // issued before on this in-order queue
                 const uint32_t k0 = ptx::smem_u32(sm.k[s0]);
-                issue_qk(tmem + col_s(0), q_s[0], k0);
+                issue_qk<kIdQk>(tmem + col_s(0), q_s[0], k0);
                 ptx::umma_commit(&sm.s_full[0]);
-                issue_qk(tmem + col_s(1), q_s[1], k0);
+                issue_qk<kIdQk>(tmem + col_s(1), q_s[1], k0);
                 ptx::umma_commit(&sm.s_full[1]);
                 if (n == 1) ptx::umma_commit(&sm.q_empty);
                 ptx::umma_commit(&sm.k_empty[s0]);
@@ -324,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                             break;
                         }
                         ptx::tc_fence_after();
-                        issue_pv(tmem + col_o(x), tmem + col_s(x), v_s, t > 0);
+                        issue_pv<kIdPv>(tmem + col_o(x), tmem + col_s(x), v_s, t > 0);
                         if (more) {
-                            issue_qk(tmem + col_s(x), q_s[x], k_s1);
+                            issue_qk<kIdQk>(tmem + col_s(x), q_s[x], k_s1);
                             ptx::umma_commit(&sm.s_full[x]);
                         } else {
                             ptx::umma_commit(&sm.o_done[x]);
@@ -526,13 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 }  // namespace
 
 bool tc_kernel_supports(const Params& p, bool gathered) {
-    return !p.kv_f4 && p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.q_len > 1 && !gathered &&
-           p.kv_layout == HGA_KV_FULL && p.C % 32 == 0;
+    if (p.q_len <= 1 || gathered || p.kv_layout != HGA_KV_FULL) return false;
+    if (p.kv_f4) return p.gq <= kRows;
+    return p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.C % 32 == 0;
 }
 
 cudaError_t launch_attend_tc(const Params& p, const void* q_rot, const KvSources& kv,
                              const int32_t* sel_groups, const int32_t* n_sel_groups, void* out,
                              cudaStream_t st) {
+    if (p.kv_f4)
+        return launch_attend_tc_pages(p, q_rot, kv, sel_groups, n_sel_groups, out, st);
     TcMaps maps;
     const int64_t BH = (int64_t)p.B * p.Hkv;
     bool ok = make_query_map(&maps.q, q_rot, p.B, p.q_len, p.Hq, kD, 8, 16) &&

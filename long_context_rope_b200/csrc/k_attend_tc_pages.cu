@@ -1,0 +1,620 @@
+// k_attend_tc_pages.cu -- prefill exact attention over the routed set of a 4-bit
+// store (HGA_KV_E2M1) on the 5th-generation tensor cores.
+//
+// "Technische Samenvatting: Hierarchical Global Attention (HGA)"
+// (gist.science), "Kernmechanisme" item 4: standard softmax over the bounded
+// exact token set of each query chunk.
+//
+// The plan is that of k_attend_tc.cu (a persistent CTA per SM, units of two M
+// tiles of 128 query rows that share every tile of 128 keys, S | S | O | O in
+// TMEM, P back in TMEM over S), with the tiles made from pages instead of
+// copied: four warps widen the codes of a page row to fp16, times their block
+// scales, straight into the swizzled operand tiles. Code x block scale has at
+// most 6 significant bits, so this is exact, and both products run on fp16:
+// bf16 operands would cost three more instructions per pair of elements.
+// Queries are scaled per row by a power of two to at most 2^15 and rounded to
+// fp16, the inverse goes into the row's score factor, so bf16's whole range is
+// held. P (at most 2^8, by the lazy rescaling) is rounded to fp16.
+//
+// Sixteen warps in four warpgroups, which split the registers:
+//   warps 0..3, 4..7  softmax of M tile A, B (168 registers a thread);
+//   warp 8            TMEM owner and MMA issuer; warp 9 builds the block lists
+//                     (88);
+//   warps 12..15      tiles (88): thread r owns key row r of every K and V
+//                     tile, whose next codes it holds in registers while it
+//                     widens the current ones, and a 16th of the query rows.
+// An M tile holds 128 / gq whole tokens (all gq heads of each), so any number
+// of query heads per KV head up to 128 is served; rows past that are idle.
+//
+// Rows after the span's last query, which may hold anything, read as zero. A
+// row whose key or value has a NaN scale must make NaN what sees it and
+// nothing else, but 0 x NaN would reach the queries that the causal rule
+// hides it from: its key is made NaN (the scores that see it become NaN, the
+// others are masked) and its value zero.
+#include "hga_blocks.cuh"
+#include "hga_e2m1.cuh"
+#include "hga_kernels.h"
+#include "hga_ptx.cuh"
+#include "hga_tc.cuh"
+
+namespace hga {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 168, kControlRegs = 88, kTileRegs = 88;
+static_assert(2 * kSoftmaxRegs + kControlRegs + kTileRegs <= 4 * 128,
+              "the warpgroups share the registers of the launch, 128 a thread");
+constexpr uint32_t kIdQk = ptx::idesc_f16_f32(kRows, kTileKeys, 0, 0);
+constexpr uint32_t kIdPv = ptx::idesc_f16_f32(kRows, kD, 0, 1);
+
+struct Smem {
+    alignas(1024) uint8_t q[2][kTile];
+    alignas(1024) uint8_t k[2][kTile];
+    alignas(1024) uint8_t v[2][kTile];
+    uint64_t bar_q, q_empty, qs_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_done[2], list_full[2], list_empty[2], drain;
+    uint32_t tmem_base;
+    int abort;
+    int nb[2];                                        // per list buffer
+    int blk_row[2][kMaxBlocks];
+    int blk_pos[2][kMaxBlocks];
+    int tile_last[2][kMaxBlocks / kBlocksPerTile];    // last key position of a tile, INT_MAX if partial
+    float q_down[2][2 * kRows];                       // per unit parity: 1 / scale of a query row
+    alignas(16) uint8_t stage[8][32 * 64];            // per softmax warp: 32 rows x 32 output dims
+};
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of one CTA");
+
+// How query rows map to tokens: row r of an M tile is head r % gq of its token
+// r / gq, T tokens per tile. For r < 128 and gq <= 128, r / gq is
+// (r * magic) >> 16 with magic = ceil(65536 / gq): the excess is below
+// 128 / 65536 < 1 / gq.
+struct Rows {
+    int T, magic, pairs;
+};
+__host__ __device__ __forceinline__ Rows rows_of(const Params& p) {
+    Rows w;
+    w.T = kRows / p.gq;
+    w.magic = (65536 + p.gq - 1) / p.gq;
+    w.pairs = (p.C + 2 * w.T - 1) / (2 * w.T);
+    return w;
+}
+
+// One unit = (pair of M tiles, query chunk, sequence x KV head); false if no
+// token of it is in the query span.
+struct Unit {
+    int tok, jj, b, h, j;  // tok: the unit's first token within the chunk
+    int64_t bh;
+};
+
+__device__ __forceinline__ bool unit_at(const Params& p, const Rows& w, int u, Unit& un) {
+    un.tok = u % w.pairs * 2 * w.T;
+    const int rest = u / w.pairs;
+    un.jj = rest % p.nQC;
+    un.bh = rest / p.nQC;
+    un.b = (int)(un.bh / p.Hkv);
+    un.h = (int)(un.bh % p.Hkv);
+    un.j = p.j0 + un.jj;
+    const int t0 = un.j * p.C + un.tok;
+    const int t1 = min(t0 + 2 * w.T, (un.j + 1) * p.C);
+    return t0 < p.q_begin + p.q_len && t1 > p.q_begin;
+}
+
+// Row r of M tile x: its position, or -1 if it holds no query of the span.
+__device__ __forceinline__ int row_pos(const Params& p, const Rows& w, const Unit& un, int x,
+                                       int r, int* head) {
+    const int t = (r * w.magic) >> 16;
+    *head = r - t * p.gq;
+    const int tok = un.tok + x * w.T + t;
+    const int pos = un.j * p.C + tok;
+    return t < w.T && tok < p.C && pos >= p.q_begin && pos < p.q_begin + p.q_len ? pos : -1;
+}
+
+// A tile thread's share of a key or value tile: its row's codes.
+struct RowCodes {
+    uint4 c[4];
+};
+
+__device__ __forceinline__ void load_codes(RowCodes& r, const uint8_t* page, int row) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r.c[i] = __ldg(reinterpret_cast<const uint4*>(page + e2m1::code_at(row, 32 * i)));
+}
+
+// Widen a row into its place in a tile: 16-byte chunk c (dims 8c .. + 7) of row
+// r at panel c / 8, chunk (c % 8) ^ (r % 8).
+__device__ __forceinline__ void widen_row(const RowCodes& rc, uint2 scales, uint8_t* tile, int r) {
+    uint8_t* dst = tile + r * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t word = i < 2 ? scales.x : scales.y;
+        const uint32_t sc = e2m1::scales_to_f16x2((uint16_t)((i & 1) ? word >> 16 : word));
+        const uint32_t w[4] = {rc.c[i].x, rc.c[i].y, rc.c[i].z, rc.c[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t f[4];
+            e2m1::codes_to_f16x2(w[e], f);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) f[z] = e2m1::hmul2_half(f[z], sc, e >> 1);
+            const int c = 4 * i + e;
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * kPanel + (((c & 7) ^ (r & 7)) << 4)) =
+                make_uint4(f[0], f[1], f[2], f[3]);
+        }
+    }
+}
+
+// True if one of the row's eight scale codes is NaN.
+__device__ __forceinline__ bool has_nan_scale(uint2 s) {
+    return (__vcmpeq4(s.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(s.y & 0x7f7f7f7fu, 0x7f7f7f7fu)) !=
+           0u;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
+    const __grid_constant__ Params p, const __nv_bfloat16* __restrict__ q,
+    const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
+    const int32_t* __restrict__ sel, const int32_t* __restrict__ nsel,
+    __nv_bfloat16* __restrict__ out, int n_units) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(align_smem_1024(smem_raw));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int span_end = p.q_begin + p.q_len;
+    const Rows rows = rows_of(p);
+
+    if (tid == 0) {
+        sm.abort = 0;
+        ptx::mbar_init(&sm.bar_q, 4);  // four tile warps
+        ptx::mbar_init(&sm.q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&sm.qs_full[s], 4);
+            ptx::mbar_init(&sm.k_full[s], 4);
+            ptx::mbar_init(&sm.k_empty[s], 1);
+            ptx::mbar_init(&sm.v_full[s], 4);
+            ptx::mbar_init(&sm.v_empty[s], 1);
+            ptx::mbar_init(&sm.s_full[s], 1);
+            ptx::mbar_init(&sm.p_full[s], 4);
+            ptx::mbar_init(&sm.o_done[s], 1);
+            ptx::mbar_init(&sm.list_full[s], 1);
+            ptx::mbar_init(&sm.list_empty[s], 12);  // tile and softmax warps
+        }
+        ptx::mbar_init(&sm.drain, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == 8) {
+        ptx::tmem_alloc(&sm.tmem_base, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int* abort = &sm.abort;
+    auto n_tiles_of = [](int nb) { return (nb + kBlocksPerTile - 1) / kBlocksPerTile; };
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, p.wait_ns)) != 0;
+    };
+
+    if (warp >= 12) {
+        // ------------------------------------------------------ tiles
+        ptx::regs_dec<kTileRegs>();
+        const int r = tid - 12 * 32;     // key row of a tile
+        const int row = r & (kGroupRows - 1);
+        int k = 0, g0 = 0;
+        Unit un;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
+            if (!unit_at(p, rows, u, un)) continue;
+            const int bf = k & 1;
+            if (!wait_warp(&sm.list_full[bf], (k >> 1) & 1)) break;
+            const int nb = sm.nb[bf], n = n_tiles_of(nb);
+            const uint8_t* kbase = ks + un.bh * p.kv_slab;
+            const uint8_t* vbase = vs + un.bh * p.kv_slab;
+            // this row's page in tile t; the pad blocks of the last tile read a page that is there
+            auto page_of = [&](int t, bool* live) {
+                const int blk = t * kBlocksPerTile + (r >> 4);
+                const int pos = sm.blk_pos[bf][blk < nb ? blk : 0];
+                *live = blk < nb && pos + row < span_end;
+                return (int64_t)(pos / kGroupRows) * kE2m1Page;
+            };
+            RowCodes kc, vc;
+            uint2 sk, sv, sv_next;
+            auto load_k = [&](int t) {
+                bool live;
+                const int64_t at = page_of(t, &live);
+                load_codes(kc, kbase + at, row);
+                const uint2 zero = make_uint2(0u, 0u);
+                sk = live ? __ldg(reinterpret_cast<const uint2*>(kbase + at + e2m1::scale_at(row, 0)))
+                          : zero;
+                sv_next =
+                    live ? __ldg(reinterpret_cast<const uint2*>(vbase + at + e2m1::scale_at(row, 0)))
+                         : zero;
+            };
+            auto load_v = [&](int t) {
+                bool live;
+                load_codes(vc, vbase + page_of(t, &live), row);
+            };
+            auto arrive = [&](uint64_t* bar) {
+                ptx::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar);
+            };
+            load_k(0);
+            load_v(0);
+            for (int t = 0; t < n; ++t) {
+                const int g = g0 + t, s = g & 1;
+                if (g >= 2 && !wait_warp(&sm.k_empty[s], ((g >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                sv = sv_next;
+                if (has_nan_scale(sv)) {
+                    sv = make_uint2(0u, 0u);
+                    sk = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+                }
+                widen_row(kc, sk, sm.k[s], r);
+                arrive(&sm.k_full[s]);
+                if (t + 1 < n) load_k(t + 1);
+                if (t == 0) {
+                    // the unit's queries: 16 lanes per row, 16 bytes each
+                    if (k >= 1 && !wait_warp(&sm.q_empty, (k - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int c = r & 15;
+                    constexpr int kBatch = 4;
+                    for (int i0 = 0; i0 < 2 * kRows / 8; i0 += kBatch) {
+                        uint4 raw[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int qr = (r >> 4) + 8 * (i0 + i);
+                            int head;
+                            const int pos = row_pos(p, rows, un, qr >> 7, qr & 127, &head);
+                            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (pos >= 0)
+                                raw[i] = __ldg(reinterpret_cast<const uint4*>(
+                                    q + (((int64_t)un.b * p.q_len + (pos - p.q_begin)) * p.Hq +
+                                         (int64_t)un.h * p.gq + head) * kD + 8 * c));
+                        }
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int qr = (r >> 4) + 8 * (i0 + i);
+                            // the row's largest exponent, over its 16 lanes
+                            uint32_t m = __vmaxu2(
+                                __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+                            uint32_t big = max(m >> 23, (m >> 7) & 0xffu);
+#pragma unroll
+                            for (int o = 1; o < 16; o <<= 1)
+                                big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            // 2^(141 - big), at most 2^100; 1 for infinities and NaN
+                            const int e = big == 255u ? 0 : min(141 - (int)big, 100);
+                            const float up = __int_as_float((e + 127) << 23);
+                            if (c == 0) sm.q_down[bf][qr] = __int_as_float((127 - e) << 23);
+                            float f[8];
+                            bf16x8_to_f32(raw[i], f);
+                            uint32_t h[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const __half2 hv = __floats2half2_rn(f[2 * z] * up, f[2 * z + 1] * up);
+                                h[z] = *reinterpret_cast<const uint32_t*>(&hv);
+                            }
+                            const int rr = qr & 127;
+                            *reinterpret_cast<uint4*>(sm.q[qr >> 7] + (c >> 3) * kPanel + rr * 128 +
+                                                      (((c & 7) ^ (rr & 7)) << 4)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                    arrive(&sm.bar_q);
+                    if (lane == 0) ptx::mbar_arrive(&sm.qs_full[bf]);
+                }
+                if (g >= 2 && !wait_warp(&sm.v_empty[s], ((g >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                widen_row(vc, sv, sm.v[s], r);
+                arrive(&sm.v_full[s]);
+                if (t + 1 < n) load_v(t + 1);
+            }
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive(&sm.list_empty[bf]);
+            g0 += n;
+            ++k;
+        }
+    } else if (warp >= 8) {
+        ptx::regs_dec<kControlRegs>();
+        if (warp == 9) {
+            // -------------------------------------------------- block lists
+            // builds the key-block list of this CTA's next units into a double buffer
+            int k = 0;
+            Unit un;
+            for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+                if (!unit_at(p, rows, u, un)) continue;
+                const int bf = k & 1;
+                if (k >= 2 && !wait_warp(&sm.list_empty[bf], ((k >> 1) - 1) & 1)) break;
+                const int64_t prob = un.bh * p.nQC + un.jj;
+                const int nb = build_key_blocks_warp(p, un.j, sel + prob * p.kg, nsel + prob, false,
+                                                     sm.blk_row[bf], sm.blk_pos[bf]);
+                __syncwarp();
+                for (int t = lane; t * kBlocksPerTile < nb; t += 32) {
+                    int last = 0;
+#pragma unroll
+                    for (int i = 0; i < kBlocksPerTile; ++i) {
+                        const int blk = t * kBlocksPerTile + i;
+                        last = blk < nb ? max(last, sm.blk_pos[bf][blk] + kGroupRows - 1) : INT_MAX;
+                    }
+                    sm.tile_last[bf][t] = last;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    sm.nb[bf] = nb;
+                    ptx::mbar_arrive(&sm.list_full[bf]);
+                }
+                ++k;
+            }
+        } else if (warp == 8 && lane == 0) {
+            // -------------------------------------------------- MMA issuer
+            const uint32_t q_s[2] = {ptx::smem_u32(sm.q[0]), ptx::smem_u32(sm.q[1])};
+            int k = 0, g0 = 0;
+            Unit un;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
+                if (!unit_at(p, rows, u, un)) continue;
+                const int bf = k & 1;
+                ok = wait_bar(&sm.list_full[bf], (k >> 1) & 1, abort, p.wait_ns);
+                if (!ok) break;
+                const int n = n_tiles_of(sm.nb[bf]);
+                const int s0 = g0 & 1;
+                ok = wait_bar(&sm.bar_q, k & 1, abort, p.wait_ns) &&
+                     wait_bar(&sm.k_full[s0], (g0 >> 1) & 1, abort, p.wait_ns);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                // S_x of the previous unit was read and its P consumed by the PV
+                // issued before on this in-order queue
+                const uint32_t k0 = ptx::smem_u32(sm.k[s0]);
+                issue_qk<kIdQk>(tmem + col_s(0), q_s[0], k0);
+                ptx::umma_commit(&sm.s_full[0]);
+                issue_qk<kIdQk>(tmem + col_s(1), q_s[1], k0);
+                ptx::umma_commit(&sm.s_full[1]);
+                if (n == 1) ptx::umma_commit(&sm.q_empty);
+                ptx::umma_commit(&sm.k_empty[s0]);
+                for (int t = 0; ok && t < n; ++t) {
+                    const int g = g0 + t, s = g & 1, s1 = (g + 1) & 1;
+                    const bool more = t + 1 < n;
+                    ok = wait_bar(&sm.v_full[s], (g >> 1) & 1, abort, p.wait_ns) &&
+                         (!more || wait_bar(&sm.k_full[s1], ((g + 1) >> 1) & 1, abort, p.wait_ns));
+                    if (!ok) break;
+                    const uint32_t v_s = ptx::smem_u32(sm.v[s]);
+                    const uint32_t k_s1 = ptx::smem_u32(sm.k[s1]);
+                    for (int x = 0; x < 2; ++x) {
+                        // P_x of this tile; for t == 0 this also orders the
+                        // PV that overwrites O_x after the same warps' epilogue
+                        // of the previous unit read it
+                        if (!wait_bar(&sm.p_full[x], g & 1, abort, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        issue_pv<kIdPv>(tmem + col_o(x), tmem + col_s(x), v_s, t > 0);
+                        if (more) {
+                            issue_qk<kIdQk>(tmem + col_s(x), q_s[x], k_s1);
+                            ptx::umma_commit(&sm.s_full[x]);
+                        } else {
+                            ptx::umma_commit(&sm.o_done[x]);
+                        }
+                    }
+                    if (!ok) break;
+                    if (more && t + 2 == n) ptx::umma_commit(&sm.q_empty);  // last QK issued
+                    ptx::umma_commit(&sm.v_empty[s]);
+                    if (more) ptx::umma_commit(&sm.k_empty[s1]);
+                }
+                g0 += n;
+                ++k;
+            }
+            // drain: every MMA issued above has completed before TMEM is freed
+            ptx::umma_commit(&sm.drain);
+            const uint64_t t0 = ptx::globaltimer_ns();
+            while (!ptx::mbar_try_wait(&sm.drain, 0) &&
+                   ptx::globaltimer_ns() - t0 < ptx::kDrainLimitNs) {
+            }
+        }
+    } else {
+        // ------------------------------------------------------ softmax
+        ptx::regs_inc<kSoftmaxRegs>();
+        const int x = warp >> 2;                        // M tile of this warpgroup
+        const int q4 = warp & 3;                        // TMEM lane quarter
+        const int r = q4 * 32 + lane;                   // row = TMEM lane
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const uint32_t s_addr = tmem + lane_off + col_s(x);
+        const uint32_t o_addr = tmem + lane_off + col_o(x);
+        const float sc0 = 1.4426950408889634f / sqrtf((float)kD) * p.k_scale;
+        int k = 0, g0 = 0;
+        Unit un;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
+            if (!unit_at(p, rows, u, un)) continue;
+            const int bf = k & 1;
+            if (!wait_warp(&sm.list_full[bf], (k >> 1) & 1) ||
+                !wait_warp(&sm.qs_full[bf], (k >> 1) & 1)) {
+                ok = false;
+                break;
+            }
+            const int nb = sm.nb[bf];
+            const int n = n_tiles_of(nb);
+            const int tokx = un.j * p.C + un.tok + x * rows.T;  // the M tile's first position
+            const int qpos = tokx + ((r * rows.magic) >> 16);
+            const float sc = sc0 * sm.q_down[bf][x * kRows + r];
+            float m_used = -INFINITY, l = 0.f;
+            for (int t = 0; t < n; ++t) {
+                const int g = g0 + t;
+                if (!wait_warp(&sm.s_full[x], g & 1)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                float sx[kTileKeys];
+                {
+                    uint32_t* xr = reinterpret_cast<uint32_t*>(sx);
+                    ptx::tmem_ld64(s_addr, xr);
+                    ptx::tmem_ld64(s_addr + 64, xr + 64);
+                    ptx::tmem_wait_ld();
+                    ptx::reg_fence<kTileKeys>(xr);
+                }
+                // mask (causal within the current chunk; padding past the set)
+                const int blk0 = t * kBlocksPerTile;
+                float mraw = -INFINITY;
+                if (sm.tile_last[bf][t] > tokx) {
+#pragma unroll
+                    for (int i = 0; i < kBlocksPerTile; ++i) {
+                        const int kp = blk0 + i < nb ? sm.blk_pos[bf][blk0 + i] : 0x7fffffff - 64;
+#pragma unroll
+                        for (int e = 0; e < kGroupRows; ++e) {
+                            const int c = i * kGroupRows + e;
+                            sx[c] = (kp + e <= qpos) ? sx[c] : -INFINITY;
+                            mraw = fmaxf(mraw, sx[c]);
+                        }
+                    }
+                } else {
+                    // four independent three-input chains
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kTileKeys; c += 8) {
+#pragma unroll
+                        for (int uu = 0; uu < 4; ++uu)
+                            m4[uu] = ptx::fmax3(m4[uu], sx[c + 2 * uu], sx[c + 2 * uu + 1]);
+                    }
+                    mraw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                }
+                const float m_new = fmaxf(m_used, mraw * sc);
+                bool rescale = false;
+                float alpha = 1.f;
+                if (m_new != -INFINITY) {
+                    if (m_used == -INFINITY) {
+                        m_used = m_new;
+                    } else if (m_new > m_used + kRescaleLog2) {
+                        alpha = ptx::ex2_approx(m_used - m_new);
+                        m_used = m_new;
+                        rescale = true;
+                    }
+                }
+                // P = 2^(S*sc - m), rounded to fp16; the row sum uses the rounded values
+                uint32_t pk[kTileKeys / 2];
+                float lsum0 = 0.f, lsum1 = 0.f;
+                const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+#pragma unroll
+                for (int c = 0; c < kTileKeys; c += 2) {
+                    float a0, a1;
+                    ptx::fma2_bc(sx[c], sx[c + 1], sc, neg_m, a0, a1);
+                    const float p0 = ptx::ex2_approx(a0);
+                    const float p1 = ptx::ex2_approx(a1);
+                    const __half2 h2 = __floats2half2_rn(p0, p1);
+                    pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                    ptx::add_f16x2_f32(pk[c / 2], lsum0, lsum1);
+                }
+                const float lsum = lsum0 + lsum1;
+                // tcgen05.ld/st are warp-collective: the whole warp rescales its
+                // rows when any row needs it (rows that do not use alpha = 1).
+                // PV of the previous tile has completed: S of this tile was issued
+                // after it on the same (in-order) tensor-core queue.
+                if (__any_sync(0xffffffffu, rescale && t >= 1)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(o_addr + 32 * c, o);
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence<32>(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        ptx::tmem_st32(o_addr + 32 * c, o);
+                    }
+                }
+                l = l * alpha + lsum;
+                ptx::tmem_st32(s_addr, pk);
+                ptx::tmem_st32(s_addr + 32, pk + 32);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sm.p_full[x]);
+            }
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive(&sm.list_empty[bf]);
+            if (!wait_warp(&sm.o_done[x], k & 1)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            // a row that met a NaN score has NaN in O, whatever its sum
+            const float inv = l > 0.f ? p.v_scale / l : 0.f;
+            // all of O in one round trip
+            uint32_t o[kD];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(o_addr + 32 * c, o + 32 * c);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence<kD>(o);
+            ptx::tc_fence_before();
+            // Coalesced output: four rounds of 32 dims; each row's 64 bytes go
+            // through this warp's staging area (16-byte chunks XOR-swizzled by
+            // (row / 2) % 4) and come back as 8 rows x 4 chunks per store.
+            uint8_t* stg = sm.stage[warp];
+            const int rr = lane >> 2, cc = lane & 3;   // read-back: row within 8, chunk
+#pragma unroll
+            for (int qd = 0; qd < 4; ++qd) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float f[8];
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) f[z] = __uint_as_float(o[32 * qd + 8 * c + z]) * inv;
+                    *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                        f32x8_to_bf16(f);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int R = 8 * i + rr;                       // row within the warp
+                    int head;
+                    const int qp = row_pos(p, rows, un, x, q4 * 32 + R, &head);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stg + R * 64 + ((cc ^ ((R >> 1) & 3)) << 4));
+                    if (qp >= 0) {
+                        __nv_bfloat16* dst = out + (((int64_t)un.b * p.q_len + (qp - p.q_begin)) * p.Hq +
+                                                    (int64_t)un.h * p.gq + head) * kD + 32 * qd + 8 * cc;
+                        *reinterpret_cast<uint4*>(dst) = v;
+                    }
+                }
+                __syncwarp();
+            }
+            g0 += n;
+            ++k;
+        }
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (*abort && tid == 0) raise_timeout(p);
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tc_pages(const Params& p, const void* q_rot, const KvSources& kv,
+                                   const int32_t* sel_groups, const int32_t* n_sel_groups,
+                                   void* out, cudaStream_t st) {
+    const size_t smem = sizeof(Smem) + 1024;
+    cudaError_t e = set_func_attr_once((const void*)attend_tc_pages_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    const int64_t n_units = (int64_t)rows_of(p).pairs * p.nQC * p.B * p.Hkv;
+    if (n_units > INT32_MAX - 65536) return cudaErrorInvalidValue;
+    const int grid = (int)(n_units < sms ? n_units : sms);
+    attend_tc_pages_kernel<<<grid, kThreads, smem, st>>>(
+        p, (const __nv_bfloat16*)q_rot, (const uint8_t*)kv.k_res, (const uint8_t*)kv.v_res,
+        sel_groups, n_sel_groups, (__nv_bfloat16*)out, (int)n_units);
+    return cudaGetLastError();
+}
+
+}  // namespace hga
