@@ -105,6 +105,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src_gm
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src_gmem)
                  : "memory");
 }
+// The same, or 16 zero bytes (the address is then not read).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src_gmem,
+                                                   bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src_gmem),
+                 "r"(copy ? 16 : 0)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }

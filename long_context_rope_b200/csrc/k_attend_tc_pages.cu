@@ -17,12 +17,13 @@
 // held. P (at most 2^8, by the lazy rescaling) is rounded to fp16.
 //
 // Sixteen warps in four warpgroups, which split the registers:
-//   warps 0..3, 4..7  softmax of M tile A, B (168 registers a thread);
+//   warps 0..3, 4..7  softmax of M tile A, B (152 registers a thread);
 //   warp 8            TMEM owner and MMA issuer; warp 9 builds the block lists
-//                     (88);
-//   warps 12..15      tiles (88): thread r owns key row r of every K and V
+//                     (104) and fetches their query rows into L2;
+//   warps 12..15      tiles (104): thread r owns key row r of every K and V
 //                     tile, whose next codes it holds in registers while it
-//                     widens the current ones, and a 16th of the query rows.
+//                     widens the current ones, and query row r of both M
+//                     tiles, which it widens in place once they are copied.
 // An M tile holds 128 / gq whole tokens (all gq heads of each), so any number
 // of query heads per KV head up to 128 is served; rows past that are idle.
 //
@@ -44,7 +45,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 168, kControlRegs = 88, kTileRegs = 88;
+constexpr int kSoftmaxRegs = 152, kControlRegs = 104, kTileRegs = 104;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kTileRegs <= 4 * 128,
               "the warpgroups share the registers of the launch, 128 a thread");
 constexpr uint32_t kIdQk = ptx::idesc_f16_f32(kRows, kTileKeys, 0, 0);
@@ -54,7 +55,7 @@ struct Smem {
     alignas(1024) uint8_t q[2][kTile];
     alignas(1024) uint8_t k[2][kTile];
     alignas(1024) uint8_t v[2][kTile];
-    uint64_t bar_q, q_empty, qs_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t bar_q, q_empty, q_in, qs_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2], list_full[2], list_empty[2], drain;
     uint32_t tmem_base;
     int abort;
@@ -102,14 +103,15 @@ __device__ __forceinline__ bool unit_at(const Params& p, const Rows& w, int u, U
     return t0 < p.q_begin + p.q_len && t1 > p.q_begin;
 }
 
-// Row r of M tile x: its position, or -1 if it holds no query of the span.
-__device__ __forceinline__ int row_pos(const Params& p, const Rows& w, const Unit& un, int x,
-                                       int r, int* head) {
+// Row r of M tile x: its offset in rows of d from head 0 (of the KV head) of the
+// chunk's first token, or -1 if it holds no query of the span. In a query span
+// of under 2^31 rows a chunk's rows fit an int.
+__device__ __forceinline__ int row_offset(const Params& p, const Rows& w, const Unit& un, int x,
+                                          int r) {
     const int t = (r * w.magic) >> 16;
-    *head = r - t * p.gq;
-    const int tok = un.tok + x * w.T + t;
-    const int pos = un.j * p.C + tok;
-    return t < w.T && tok < p.C && pos >= p.q_begin && pos < p.q_begin + p.q_len ? pos : -1;
+    const int tok = un.tok + x * w.T + t, pos = un.j * p.C + tok;
+    const bool ok = t < w.T && tok < p.C && pos >= p.q_begin && pos < p.q_begin + p.q_len;
+    return ok ? tok * p.Hq + (r - t * p.gq) : -1;
 }
 
 // A tile thread's share of a key or value tile: its row's codes.
@@ -145,6 +147,62 @@ __device__ __forceinline__ void widen_row(const RowCodes& rc, uint2 scales, uint
     }
 }
 
+// Asynchronous copies of a unit's query rows (bf16) into their places in the
+// operand tiles: 16 lanes a row, zeros for rows without a query. r: the tile
+// thread, 0 .. 127.
+__device__ __forceinline__ void copy_queries(const Params& p, const Rows& w, const Unit& un,
+                                             const __nv_bfloat16* q, uint8_t (*tiles)[kTile],
+                                             int r) {
+    const int c = r & 15;
+    const uint32_t dst = ptx::smem_u32(tiles[0]) + (c >> 3) * kPanel;
+    const __nv_bfloat16* src = q + (((int64_t)un.b * p.q_len + (un.j * p.C - p.q_begin)) * p.Hq +
+                                    (int64_t)un.h * p.gq) * kD + 8 * c;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll 4
+        for (int i = 0; i < kRows / 8; ++i) {
+            const int rr = (r >> 4) + 8 * i;
+            const int off = row_offset(p, w, un, x, rr);
+            ptx::cp_async16_or_zero(dst + x * kTile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+                                    off >= 0 ? src + (int64_t)off * kD : q, off >= 0);
+        }
+    ptx::cp_async_commit();
+}
+
+// Row r of a query tile from bf16 to fp16 in place, scaled by a power of two;
+// returns the inverse of the scale.
+__device__ __forceinline__ float scale_row(uint8_t* tile, int r) {
+    uint8_t* base = tile + r * 128;
+    auto at = [&](int c) {
+        return reinterpret_cast<uint4*>(base + (c >> 3) * kPanel + (((c & 7) ^ (r & 7)) << 4));
+    };
+    uint32_t m = 0u;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const uint4 v = *at(c);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    // the largest exponent field; the scale is 2^(141 - big), at most 2^100, or
+    // 1 for infinities and NaN
+    const uint32_t big = max(m >> 23, (m >> 7) & 0xffu);
+    const int e = big == 255u ? 0 : min(141 - (int)big, 100);
+    const float up = __int_as_float((e + 127) << 23);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        float f[8];
+        bf16x8_to_f32(*at(c), f);
+        uint32_t h[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const __half2 hv = __floats2half2_rn(f[2 * z] * up, f[2 * z + 1] * up);
+            h[z] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        *at(c) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return __int_as_float((127 - e) << 23);
+}
+
 // True if one of the row's eight scale codes is NaN.
 __device__ __forceinline__ bool has_nan_scale(uint2 s) {
     return (__vcmpeq4(s.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(s.y & 0x7f7f7f7fu, 0x7f7f7f7fu)) !=
@@ -166,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
         sm.abort = 0;
         ptx::mbar_init(&sm.bar_q, 4);  // four tile warps
         ptx::mbar_init(&sm.q_empty, 1);
+        ptx::mbar_init(&sm.q_in, 4);
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&sm.qs_full[s], 4);
             ptx::mbar_init(&sm.k_full[s], 4);
@@ -256,57 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                 arrive(&sm.k_full[s]);
                 if (t + 1 < n) load_k(t + 1);
                 if (t == 0) {
-                    // the unit's queries: 16 lanes per row, 16 bytes each
                     if (k >= 1 && !wait_warp(&sm.q_empty, (k - 1) & 1)) {
                         ok = false;
                         break;
                     }
-                    const int c = r & 15;
-                    constexpr int kBatch = 4;
-                    for (int i0 = 0; i0 < 2 * kRows / 8; i0 += kBatch) {
-                        uint4 raw[kBatch];
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            const int qr = (r >> 4) + 8 * (i0 + i);
-                            int head;
-                            const int pos = row_pos(p, rows, un, qr >> 7, qr & 127, &head);
-                            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-                            if (pos >= 0)
-                                raw[i] = __ldg(reinterpret_cast<const uint4*>(
-                                    q + (((int64_t)un.b * p.q_len + (pos - p.q_begin)) * p.Hq +
-                                         (int64_t)un.h * p.gq + head) * kD + 8 * c));
-                        }
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            const int qr = (r >> 4) + 8 * (i0 + i);
-                            // the row's largest exponent, over its 16 lanes
-                            uint32_t m = __vmaxu2(
-                                __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                                __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
-                            uint32_t big = max(m >> 23, (m >> 7) & 0xffu);
-#pragma unroll
-                            for (int o = 1; o < 16; o <<= 1)
-                                big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                            // 2^(141 - big), at most 2^100; 1 for infinities and NaN
-                            const int e = big == 255u ? 0 : min(141 - (int)big, 100);
-                            const float up = __int_as_float((e + 127) << 23);
-                            if (c == 0) sm.q_down[bf][qr] = __int_as_float((127 - e) << 23);
-                            float f[8];
-                            bf16x8_to_f32(raw[i], f);
-                            uint32_t h[4];
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                const __half2 hv = __floats2half2_rn(f[2 * z] * up, f[2 * z + 1] * up);
-                                h[z] = *reinterpret_cast<const uint32_t*>(&hv);
-                            }
-                            const int rr = qr & 127;
-                            *reinterpret_cast<uint4*>(sm.q[qr >> 7] + (c >> 3) * kPanel + rr * 128 +
-                                                      (((c & 7) ^ (rr & 7)) << 4)) =
-                                make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                    }
-                    arrive(&sm.bar_q);
-                    if (lane == 0) ptx::mbar_arrive(&sm.qs_full[bf]);
+                    copy_queries(p, rows, un, q, sm.q, r);
                 }
                 if (g >= 2 && !wait_warp(&sm.v_empty[s], ((g >> 1) - 1) & 1)) {
                     ok = false;
@@ -315,12 +328,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                 widen_row(vc, sv, sm.v[s], r);
                 arrive(&sm.v_full[s]);
                 if (t + 1 < n) load_v(t + 1);
+                if (t == 0) {
+                    ptx::cp_async_wait<0>();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sm.q_in);
+                    if (!wait_warp(&sm.q_in, k & 1)) {  // every tile thread's copies are in
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        sm.q_down[bf][x * kRows + r] = scale_row(sm.q[x], r);
+                    arrive(&sm.bar_q);
+                    if (lane == 0) ptx::mbar_arrive(&sm.qs_full[bf]);
+                }
             }
             if (!ok) break;
             if (lane == 0) ptx::mbar_arrive(&sm.list_empty[bf]);
             g0 += n;
             ++k;
         }
+        ptx::cp_async_wait<0>();  // nothing in flight into this CTA's memory when it exits
     } else if (warp >= 8) {
         ptx::regs_dec<kControlRegs>();
         if (warp == 9) {
@@ -349,6 +377,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                 if (lane == 0) {
                     sm.nb[bf] = nb;
                     ptx::mbar_arrive(&sm.list_full[bf]);
+                }
+                // a token's heads are contiguous
+                for (int i = lane; i < 2 * rows.T; i += 32) {
+                    const int off = row_offset(p, rows, un, i / rows.T, i % rows.T * p.gq);
+                    if (off >= 0)
+                        ptx::bulk_prefetch_l2(
+                            q + (((int64_t)un.b * p.q_len + (un.j * p.C - p.q_begin)) * p.Hq +
+                                 (int64_t)un.h * p.gq + off) * kD,
+                            (uint32_t)(p.gq * kD * 2));
                 }
                 ++k;
             }
@@ -452,64 +489,83 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                     break;
                 }
                 ptx::tc_fence_after();
-                float sx[kTileKeys];
-                {
-                    uint32_t* xr = reinterpret_cast<uint32_t*>(sx);
-                    ptx::tmem_ld64(s_addr, xr);
-                    ptx::tmem_ld64(s_addr + 64, xr + 64);
-                    ptx::tmem_wait_ld();
-                    ptx::reg_fence<kTileKeys>(xr);
-                }
-                // mask (causal within the current chunk; padding past the set)
                 const int blk0 = t * kBlocksPerTile;
-                float mraw = -INFINITY;
-                if (sm.tile_last[bf][t] > tokx) {
+                const bool masked = sm.tile_last[bf][t] > tokx;
+                // the scores in four chunks of 32 keys, the next one on its way while
+                // one is worked on; masked (causal within the current chunk, padding
+                // past the set); f takes a chunk's number and scores
+                auto chunks = [&](auto f) {
+                    uint32_t buf[2][32];
+                    ptx::tmem_ld32(s_addr, buf[0]);
 #pragma unroll
-                    for (int i = 0; i < kBlocksPerTile; ++i) {
-                        const int kp = blk0 + i < nb ? sm.blk_pos[bf][blk0 + i] : 0x7fffffff - 64;
+                    for (int c = 0; c < 4; ++c) {
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence<32>(buf[c & 1]);
+                        if (c < 3) ptx::tmem_ld32(s_addr + 32 * (c + 1), buf[(c + 1) & 1]);
+                        float* sx = reinterpret_cast<float*>(buf[c & 1]);
+                        if (masked) {
 #pragma unroll
-                        for (int e = 0; e < kGroupRows; ++e) {
-                            const int c = i * kGroupRows + e;
-                            sx[c] = (kp + e <= qpos) ? sx[c] : -INFINITY;
-                            mraw = fmaxf(mraw, sx[c]);
+                            for (int i = 0; i < 2; ++i) {
+                                const int blk = blk0 + 2 * c + i;
+                                const int see = blk < nb ? qpos - sm.blk_pos[bf][blk] : -1;
+#pragma unroll
+                                for (int e = 0; e < kGroupRows; ++e)
+                                    if (e > see) sx[16 * i + e] = -INFINITY;
+                            }
                         }
+                        f(c, sx);
                     }
-                } else {
-                    // four independent three-input chains
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                };
+                // the row's largest score: four independent three-input chains
+                auto chunk_max = [&](const float* sx, float (&m4)[4]) {
 #pragma unroll
-                    for (int c = 0; c < kTileKeys; c += 8) {
+                    for (int e = 0; e < 32; e += 8)
 #pragma unroll
                         for (int uu = 0; uu < 4; ++uu)
-                            m4[uu] = ptx::fmax3(m4[uu], sx[c + 2 * uu], sx[c + 2 * uu + 1]);
-                    }
-                    mraw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            m4[uu] = ptx::fmax3(m4[uu], sx[e + 2 * uu], sx[e + 2 * uu + 1]);
+                };
+                auto join_max = [&](const float (&m4)[4]) {
+                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                };
+                if (t == 0) {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    chunks([&](int, const float* sx) { chunk_max(sx, m4); });
+                    m_used = fmaxf(m_used, join_max(m4));
                 }
-                const float m_new = fmaxf(m_used, mraw * sc);
+                // P = 2^(S*sc - m), rounded to fp16, the row sum of the rounded values,
+                // and this tile's maximum on the side
+                uint32_t pk[kTileKeys / 2];
+                float lsum0, lsum1, m_tile;
+                auto weights = [&]() {
+                    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    lsum0 = lsum1 = 0.f;
+                    chunks([&](int c, const float* sx) {
+                        chunk_max(sx, m4);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a0, a1;
+                            ptx::fma2_bc(sx[e], sx[e + 1], sc, neg_m, a0, a1);
+                            const __half2 h2 =
+                                __floats2half2_rn(ptx::ex2_approx(a0), ptx::ex2_approx(a1));
+                            pk[16 * c + e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                            ptx::add_f16x2_f32(pk[16 * c + e / 2], lsum0, lsum1);
+                        }
+                    });
+                    m_tile = join_max(m4);
+                };
+                weights();
+                // seldom: a maximum more than 2^8 above the one used; the rows that
+                // have one take it, and the tile is done again
                 bool rescale = false;
                 float alpha = 1.f;
-                if (m_new != -INFINITY) {
-                    if (m_used == -INFINITY) {
-                        m_used = m_new;
-                    } else if (m_new > m_used + kRescaleLog2) {
-                        alpha = ptx::ex2_approx(m_used - m_new);
-                        m_used = m_new;
+                if (__any_sync(0xffffffffu, m_tile > m_used + kRescaleLog2)) {
+                    if (m_tile > m_used + kRescaleLog2) {
+                        alpha = ptx::ex2_approx(m_used - m_tile);
+                        m_used = m_tile;
                         rescale = true;
                     }
-                }
-                // P = 2^(S*sc - m), rounded to fp16; the row sum uses the rounded values
-                uint32_t pk[kTileKeys / 2];
-                float lsum0 = 0.f, lsum1 = 0.f;
-                const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-#pragma unroll
-                for (int c = 0; c < kTileKeys; c += 2) {
-                    float a0, a1;
-                    ptx::fma2_bc(sx[c], sx[c + 1], sc, neg_m, a0, a1);
-                    const float p0 = ptx::ex2_approx(a0);
-                    const float p1 = ptx::ex2_approx(a1);
-                    const __half2 h2 = __floats2half2_rn(p0, p1);
-                    pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-                    ptx::add_f16x2_f32(pk[c / 2], lsum0, lsum1);
+                    weights();
                 }
                 const float lsum = lsum0 + lsum1;
                 // tcgen05.ld/st are warp-collective: the whole warp rescales its
@@ -545,6 +601,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
             ptx::tc_fence_after();
             // a row that met a NaN score has NaN in O, whatever its sum
             const float inv = l > 0.f ? p.v_scale / l : 0.f;
+            // where this lane's read-back rows go: row 8i + lane / 4 of the warp
+            const int rr = lane >> 2, cc = lane & 3;
+            __nv_bfloat16* obase =
+                out + (((int64_t)un.b * p.q_len + (un.j * p.C - p.q_begin)) * p.Hq +
+                       (int64_t)un.h * p.gq) * kD + 8 * cc;
+            int off[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off[i] = row_offset(p, rows, un, x, q4 * 32 + 8 * i + rr);
             // all of O in one round trip
             uint32_t o[kD];
 #pragma unroll
@@ -556,7 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
             // through this warp's staging area (16-byte chunks XOR-swizzled by
             // (row / 2) % 4) and come back as 8 rows x 4 chunks per store.
             uint8_t* stg = sm.stage[warp];
-            const int rr = lane >> 2, cc = lane & 3;   // read-back: row within 8, chunk
 #pragma unroll
             for (int qd = 0; qd < 4; ++qd) {
 #pragma unroll
@@ -571,14 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int R = 8 * i + rr;                       // row within the warp
-                    int head;
-                    const int qp = row_pos(p, rows, un, x, q4 * 32 + R, &head);
                     const uint4 v = *reinterpret_cast<const uint4*>(stg + R * 64 + ((cc ^ ((R >> 1) & 3)) << 4));
-                    if (qp >= 0) {
-                        __nv_bfloat16* dst = out + (((int64_t)un.b * p.q_len + (qp - p.q_begin)) * p.Hq +
-                                                    (int64_t)un.h * p.gq + head) * kD + 32 * qd + 8 * cc;
-                        *reinterpret_cast<uint4*>(dst) = v;
-                    }
+                    if (off[i] >= 0) *reinterpret_cast<uint4*>(obase + (int64_t)off[i] * kD + 32 * qd) = v;
                 }
                 __syncwarp();
             }
