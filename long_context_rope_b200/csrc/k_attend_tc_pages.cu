@@ -8,22 +8,22 @@
 // The plan is that of k_attend_tc.cu (a persistent CTA per SM, units of two M
 // tiles of 128 query rows that share every tile of 128 keys, S | S | O | O in
 // TMEM, P back in TMEM over S), with the tiles made from pages instead of
-// copied: four warps widen the codes of a page row to fp16, times their block
-// scales, straight into the swizzled operand tiles. Code x block scale has at
-// most 6 significant bits, so this is exact, and both products run on fp16:
-// bf16 operands would cost three more instructions per pair of elements.
-// Queries are scaled per row by a power of two to at most 2^15 and rounded to
-// fp16, the inverse goes into the row's score factor, so bf16's whole range is
-// held. P (at most 2^8, by the lazy rescaling) is rounded to fp16.
+// copied: four warps widen the codes of a page row to 16 bits, times their
+// block scales, straight into the swizzled operand tiles. Code x block scale
+// has at most 6 significant bits, so that is exact in either type. Keys become
+// bf16, the queries' type (three more instructions per pair of elements than
+// fp16, but queries in fp16 would have to be scaled row by row to keep bf16's
+// range, which held up every unit's start: 571 us for the last 16K tokens of
+// 32K). Values become fp16, and so does P (at most 2^8, by the lazy rescaling).
 //
 // Sixteen warps in four warpgroups, which split the registers:
 //   warps 0..3, 4..7  softmax of M tile A, B (152 registers a thread);
 //   warp 8            TMEM owner and MMA issuer; warp 9 builds the block lists
-//                     (104) and fetches their query rows into L2;
+//                     and fetches their query rows into L2; warps 10, 11 copy
+//                     the query rows (104);
 //   warps 12..15      tiles (104): thread r owns key row r of every K and V
 //                     tile, whose next codes it holds in registers while it
-//                     widens the current ones, and query row r of both M
-//                     tiles, which it widens in place once they are copied.
+//                     widens the current ones.
 // An M tile holds 128 / gq whole tokens (all gq heads of each), so any number
 // of query heads per KV head up to 128 is served; rows past that are idle.
 //
@@ -45,17 +45,18 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 512;
+constexpr float kMaxSum = 256.f;  // of 32 weights
 constexpr int kSoftmaxRegs = 152, kControlRegs = 104, kTileRegs = 104;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kTileRegs <= 4 * 128,
               "the warpgroups share the registers of the launch, 128 a thread");
-constexpr uint32_t kIdQk = ptx::idesc_f16_f32(kRows, kTileKeys, 0, 0);
+constexpr uint32_t kIdQk = ptx::idesc_bf16_f32(kRows, kTileKeys, 0, 0);
 constexpr uint32_t kIdPv = ptx::idesc_f16_f32(kRows, kD, 0, 1);
 
 struct Smem {
     alignas(1024) uint8_t q[2][kTile];
     alignas(1024) uint8_t k[2][kTile];
     alignas(1024) uint8_t v[2][kTile];
-    uint64_t bar_q, q_empty, q_in, qs_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t bar_q, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2], list_full[2], list_empty[2], drain;
     uint32_t tmem_base;
     int abort;
@@ -63,7 +64,6 @@ struct Smem {
     int blk_row[2][kMaxBlocks];
     int blk_pos[2][kMaxBlocks];
     int tile_last[2][kMaxBlocks / kBlocksPerTile];    // last key position of a tile, INT_MAX if partial
-    float q_down[2][2 * kRows];                       // per unit parity: 1 / scale of a query row
     alignas(16) uint8_t stage[8][32 * 64];            // per softmax warp: 32 rows x 32 output dims
 };
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of one CTA");
@@ -84,7 +84,9 @@ __host__ __device__ __forceinline__ Rows rows_of(const Params& p) {
 }
 
 // One unit = (pair of M tiles, query chunk, sequence x KV head); false if no
-// token of it is in the query span.
+// token of it is in the query span. Late chunks, which have the most keys,
+// come first: of 512 units on 148 CTAs the fullest CTA has 14 percent less to
+// do than in ascending order.
 struct Unit {
     int tok, jj, b, h, j;  // tok: the unit's first token within the chunk
     int64_t bh;
@@ -92,15 +94,22 @@ struct Unit {
 
 __device__ __forceinline__ bool unit_at(const Params& p, const Rows& w, int u, Unit& un) {
     un.tok = u % w.pairs * 2 * w.T;
-    const int rest = u / w.pairs;
-    un.jj = rest % p.nQC;
-    un.bh = rest / p.nQC;
+    const int rest = u / w.pairs, units = p.B * p.Hkv;
+    un.jj = p.nQC - 1 - rest / units;
+    un.bh = rest % units;
     un.b = (int)(un.bh / p.Hkv);
     un.h = (int)(un.bh % p.Hkv);
     un.j = p.j0 + un.jj;
     const int t0 = un.j * p.C + un.tok;
     const int t1 = min(t0 + 2 * w.T, (un.j + 1) * p.C);
     return t0 < p.q_begin + p.q_len && t1 > p.q_begin;
+}
+
+// This CTA's unit of round rd: every other round in reverse, so that the CTA
+// with the heaviest unit of one round has the lightest of the next.
+__device__ __forceinline__ int unit_in_round(int rd) {
+    const int grid = (int)gridDim.x, b = (int)blockIdx.x;
+    return rd * grid + ((rd & 1) ? grid - 1 - b : b);
 }
 
 // Row r of M tile x: its offset in rows of d from head 0 (of the KV head) of the
@@ -125,8 +134,16 @@ __device__ __forceinline__ void load_codes(RowCodes& r, const uint8_t* page, int
         r.c[i] = __ldg(reinterpret_cast<const uint4*>(page + e2m1::code_at(row, 32 * i)));
 }
 
-// Widen a row into its place in a tile: 16-byte chunk c (dims 8c .. + 7) of row
-// r at panel c / 8, chunk (c % 8) ^ (r % 8).
+// An f16 pair as a bf16 pair (exact for what code x scale can be).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Widen a row into its place in a tile, to bf16 or fp16: 16-byte chunk c (dims
+// 8c .. + 7) of row r at panel c / 8, chunk (c % 8) ^ (r % 8).
+template <bool kBf16>
 __device__ __forceinline__ void widen_row(const RowCodes& rc, uint2 scales, uint8_t* tile, int r) {
     uint8_t* dst = tile + r * 128;
 #pragma unroll
@@ -139,7 +156,10 @@ __device__ __forceinline__ void widen_row(const RowCodes& rc, uint2 scales, uint
             uint32_t f[4];
             e2m1::codes_to_f16x2(w[e], f);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) f[z] = e2m1::hmul2_half(f[z], sc, e >> 1);
+            for (int z = 0; z < 4; ++z) {
+                f[z] = e2m1::hmul2_half(f[z], sc, e >> 1);
+                if (kBf16) f[z] = f16x2_to_bf16x2(f[z]);
+            }
             const int c = 4 * i + e;
             *reinterpret_cast<uint4*>(dst + (c >> 3) * kPanel + (((c & 7) ^ (r & 7)) << 4)) =
                 make_uint4(f[0], f[1], f[2], f[3]);
@@ -147,9 +167,8 @@ __device__ __forceinline__ void widen_row(const RowCodes& rc, uint2 scales, uint
     }
 }
 
-// Asynchronous copies of a unit's query rows (bf16) into their places in the
-// operand tiles: 16 lanes a row, zeros for rows without a query. r: the tile
-// thread, 0 .. 127.
+// Asynchronous copies of a unit's query rows into their places in the operand
+// tiles: 16 lanes a row, zeros for rows without a query. r: thread 0 .. 63.
 __device__ __forceinline__ void copy_queries(const Params& p, const Rows& w, const Unit& un,
                                              const __nv_bfloat16* q, uint8_t (*tiles)[kTile],
                                              int r) {
@@ -160,47 +179,12 @@ __device__ __forceinline__ void copy_queries(const Params& p, const Rows& w, con
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll 4
-        for (int i = 0; i < kRows / 8; ++i) {
-            const int rr = (r >> 4) + 8 * i;
+        for (int i = 0; i < kRows / 4; ++i) {
+            const int rr = (r >> 4) + 4 * i;
             const int off = row_offset(p, w, un, x, rr);
             ptx::cp_async16_or_zero(dst + x * kTile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
                                     off >= 0 ? src + (int64_t)off * kD : q, off >= 0);
         }
-    ptx::cp_async_commit();
-}
-
-// Row r of a query tile from bf16 to fp16 in place, scaled by a power of two;
-// returns the inverse of the scale.
-__device__ __forceinline__ float scale_row(uint8_t* tile, int r) {
-    uint8_t* base = tile + r * 128;
-    auto at = [&](int c) {
-        return reinterpret_cast<uint4*>(base + (c >> 3) * kPanel + (((c & 7) ^ (r & 7)) << 4));
-    };
-    uint32_t m = 0u;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        const uint4 v = *at(c);
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-    }
-    // the largest exponent field; the scale is 2^(141 - big), at most 2^100, or
-    // 1 for infinities and NaN
-    const uint32_t big = max(m >> 23, (m >> 7) & 0xffu);
-    const int e = big == 255u ? 0 : min(141 - (int)big, 100);
-    const float up = __int_as_float((e + 127) << 23);
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        float f[8];
-        bf16x8_to_f32(*at(c), f);
-        uint32_t h[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            const __half2 hv = __floats2half2_rn(f[2 * z] * up, f[2 * z + 1] * up);
-            h[z] = *reinterpret_cast<const uint32_t*>(&hv);
-        }
-        *at(c) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
-    return __int_as_float((127 - e) << 23);
 }
 
 // True if one of the row's eight scale codes is NaN.
@@ -222,11 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
 
     if (tid == 0) {
         sm.abort = 0;
-        ptx::mbar_init(&sm.bar_q, 4);  // four tile warps
+        ptx::mbar_init(&sm.bar_q, 2);  // warps 10, 11
         ptx::mbar_init(&sm.q_empty, 1);
-        ptx::mbar_init(&sm.q_in, 4);
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(&sm.qs_full[s], 4);
             ptx::mbar_init(&sm.k_full[s], 4);
             ptx::mbar_init(&sm.k_empty[s], 1);
             ptx::mbar_init(&sm.v_full[s], 4);
@@ -262,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
         int k = 0, g0 = 0;
         Unit un;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
+        for (int rd = 0, u; ok && (u = unit_in_round(rd)) < n_units; ++rd) {
             if (!unit_at(p, rows, u, un)) continue;
             const int bf = k & 1;
             if (!wait_warp(&sm.list_full[bf], (k >> 1) & 1)) break;
@@ -311,44 +293,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                     sv = make_uint2(0u, 0u);
                     sk = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
                 }
-                widen_row(kc, sk, sm.k[s], r);
+                widen_row<true>(kc, sk, sm.k[s], r);
                 arrive(&sm.k_full[s]);
                 if (t + 1 < n) load_k(t + 1);
-                if (t == 0) {
-                    if (k >= 1 && !wait_warp(&sm.q_empty, (k - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    copy_queries(p, rows, un, q, sm.q, r);
-                }
                 if (g >= 2 && !wait_warp(&sm.v_empty[s], ((g >> 1) - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                widen_row(vc, sv, sm.v[s], r);
+                widen_row<false>(vc, sv, sm.v[s], r);
                 arrive(&sm.v_full[s]);
                 if (t + 1 < n) load_v(t + 1);
-                if (t == 0) {
-                    ptx::cp_async_wait<0>();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&sm.q_in);
-                    if (!wait_warp(&sm.q_in, k & 1)) {  // every tile thread's copies are in
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        sm.q_down[bf][x * kRows + r] = scale_row(sm.q[x], r);
-                    arrive(&sm.bar_q);
-                    if (lane == 0) ptx::mbar_arrive(&sm.qs_full[bf]);
-                }
             }
             if (!ok) break;
             if (lane == 0) ptx::mbar_arrive(&sm.list_empty[bf]);
             g0 += n;
             ++k;
         }
-        ptx::cp_async_wait<0>();  // nothing in flight into this CTA's memory when it exits
     } else if (warp >= 8) {
         ptx::regs_dec<kControlRegs>();
         if (warp == 9) {
@@ -356,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
             // builds the key-block list of this CTA's next units into a double buffer
             int k = 0;
             Unit un;
-            for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+            for (int rd = 0, u; (u = unit_in_round(rd)) < n_units; ++rd) {
                 if (!unit_at(p, rows, u, un)) continue;
                 const int bf = k & 1;
                 if (k >= 2 && !wait_warp(&sm.list_empty[bf], ((k >> 1) - 1) & 1)) break;
@@ -389,13 +349,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                 }
                 ++k;
             }
+        } else if (warp >= 10) {
+            // -------------------------------------------------- queries
+            int k = 0;
+            Unit un;
+            for (int rd = 0, u; (u = unit_in_round(rd)) < n_units; ++rd) {
+                if (!unit_at(p, rows, u, un)) continue;
+                if (k >= 1 && !wait_warp(&sm.q_empty, (k - 1) & 1)) break;
+                copy_queries(p, rows, un, q, sm.q, tid - 10 * 32);
+                ptx::cp_async_commit();
+                ptx::cp_async_wait<0>();
+                ptx::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sm.bar_q);
+                ++k;
+            }
         } else if (warp == 8 && lane == 0) {
             // -------------------------------------------------- MMA issuer
             const uint32_t q_s[2] = {ptx::smem_u32(sm.q[0]), ptx::smem_u32(sm.q[1])};
             int k = 0, g0 = 0;
             Unit un;
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
+            for (int rd = 0, u; ok && (u = unit_in_round(rd)) < n_units; ++rd) {
                 if (!unit_at(p, rows, u, un)) continue;
                 const int bf = k & 1;
                 ok = wait_bar(&sm.list_full[bf], (k >> 1) & 1, abort, p.wait_ns);
@@ -464,15 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const uint32_t s_addr = tmem + lane_off + col_s(x);
         const uint32_t o_addr = tmem + lane_off + col_o(x);
-        const float sc0 = 1.4426950408889634f / sqrtf((float)kD) * p.k_scale;
+        const float sc = 1.4426950408889634f / sqrtf((float)kD) * p.k_scale;
         int k = 0, g0 = 0;
         Unit un;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
+        for (int rd = 0, u; ok && (u = unit_in_round(rd)) < n_units; ++rd) {
             if (!unit_at(p, rows, u, un)) continue;
             const int bf = k & 1;
-            if (!wait_warp(&sm.list_full[bf], (k >> 1) & 1) ||
-                !wait_warp(&sm.qs_full[bf], (k >> 1) & 1)) {
+            if (!wait_warp(&sm.list_full[bf], (k >> 1) & 1)) {
                 ok = false;
                 break;
             }
@@ -480,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
             const int n = n_tiles_of(nb);
             const int tokx = un.j * p.C + un.tok + x * rows.T;  // the M tile's first position
             const int qpos = tokx + ((r * rows.magic) >> 16);
-            const float sc = sc0 * sm.q_down[bf][x * kRows + r];
             float m_used = -INFINITY, l = 0.f;
             for (int t = 0; t < n; ++t) {
                 const int g = g0 + t;
@@ -491,18 +464,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                 ptx::tc_fence_after();
                 const int blk0 = t * kBlocksPerTile;
                 const bool masked = sm.tile_last[bf][t] > tokx;
-                // the scores in four chunks of 32 keys, the next one on its way while
-                // one is worked on; masked (causal within the current chunk, padding
-                // past the set); f takes a chunk's number and scores
-                auto chunks = [&](auto f) {
-                    uint32_t buf[2][32];
-                    ptx::tmem_ld32(s_addr, buf[0]);
+                // Four chunks of 32 scores, the next one on its way while one is worked
+                // on: masked (causal within the current chunk, padding past the set),
+                // turned into P = 2^(S*sc - m) in fp16 and written over the scores of
+                // chunks already read. m is raised, to the chunk's maximum, only where
+                // a chunk's weights sum to more than 2^8 (seldom; without that no weight
+                // is above 2^8, far inside fp16) or there is no m yet; the row's weights
+                // and sum so far then shrink by alpha, and the chunk is done again. So
+                // no maximum is taken elsewhere.
+                float2 lsum = make_float2(0.f, 0.f);
+                float alpha = 1.f;
+                bool rescale = false;
+                uint32_t buf[2][32];
+                ptx::tmem_ld32(s_addr, buf[0]);
+#pragma unroll 1
+                for (int c0 = 0; c0 < 4; c0 += 2) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int z = 0; z < 2; ++z) {
+                        const int c = c0 + z;
                         ptx::tmem_wait_ld();
-                        ptx::reg_fence<32>(buf[c & 1]);
-                        if (c < 3) ptx::tmem_ld32(s_addr + 32 * (c + 1), buf[(c + 1) & 1]);
-                        float* sx = reinterpret_cast<float*>(buf[c & 1]);
+                        ptx::reg_fence<32>(buf[z]);
+                        if (c < 3) ptx::tmem_ld32(s_addr + 32 * (c + 1), buf[z ^ 1]);
+                        float* sx = reinterpret_cast<float*>(buf[z]);
                         if (masked) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
@@ -513,61 +496,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                                     if (e > see) sx[16 * i + e] = -INFINITY;
                             }
                         }
-                        f(c, sx);
-                    }
-                };
-                // the row's largest score: four independent three-input chains
-                auto chunk_max = [&](const float* sx, float (&m4)[4]) {
+                        uint32_t pk[16];
+                        float2 ls[2];
+                        for (bool again = false;; again = true) {
+                            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                            ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
+                            for (int e = 0; e < 32; e += 2) {
+                                float a0, a1;
+                                ptx::fma2_bc(sx[e], sx[e + 1], sc, neg_m, a0, a1);
+                                const float2 w =
+                                    make_float2(ptx::ex2_approx(a0), ptx::ex2_approx(a1));
+                                ls[(e >> 1) & 1] = ptx::add2(ls[(e >> 1) & 1], w);
+                                const __half2 h2 = __floats2half2_rn(w.x, w.y);
+                                pk[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                            }
+                            ls[0] = ptx::add2(ls[0], ls[1]);
+                            const bool bad = ls[0].x + ls[0].y > kMaxSum || m_used == -INFINITY;
+                            if (again || !__any_sync(0xffffffffu, bad)) break;
+                            float mc = sx[0];
 #pragma unroll
-                        for (int uu = 0; uu < 4; ++uu)
-                            m4[uu] = ptx::fmax3(m4[uu], sx[e + 2 * uu], sx[e + 2 * uu + 1]);
-                };
-                auto join_max = [&](const float (&m4)[4]) {
-                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
-                };
-                if (t == 0) {
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    chunks([&](int, const float* sx) { chunk_max(sx, m4); });
-                    m_used = fmaxf(m_used, join_max(m4));
-                }
-                // P = 2^(S*sc - m), rounded to fp16, the row sum of the rounded values,
-                // and this tile's maximum on the side
-                uint32_t pk[kTileKeys / 2];
-                float lsum0, lsum1, m_tile;
-                auto weights = [&]() {
-                    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    lsum0 = lsum1 = 0.f;
-                    chunks([&](int c, const float* sx) {
-                        chunk_max(sx, m4);
+                            for (int e = 1; e < 32; ++e) mc = fmaxf(mc, sx[e]);
+                            mc *= sc;
+                            const bool above = bad && mc > m_used;
+                            // by a whole number, so that a is a power of two
+                            const float m_new =
+                                m_used == -INFINITY ? mc : m_used + ceilf(mc - m_used);
+                            const float a = above ? ptx::ex2_approx(m_used - m_new) : 1.f;
+                            m_used = above ? m_new : m_used;
+                            alpha *= a;
+                            lsum = ptx::mul2(lsum, make_float2(a, a));
+                            rescale = true;
+                            ptx::tmem_wait_st();
+                            for (int y = 0; y < c; ++y) {
+                                uint32_t w[16];
+                                ptx::tmem_ld16(s_addr + 16 * y, w);
+                                ptx::tmem_wait_ld();
+                                ptx::reg_fence<16>(w);
+                                const __half2 a2 = __float2half2_rn(a);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a0, a1;
-                            ptx::fma2_bc(sx[e], sx[e + 1], sc, neg_m, a0, a1);
-                            const __half2 h2 =
-                                __floats2half2_rn(ptx::ex2_approx(a0), ptx::ex2_approx(a1));
-                            pk[16 * c + e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-                            ptx::add_f16x2_f32(pk[16 * c + e / 2], lsum0, lsum1);
+                                for (int e = 0; e < 16; ++e)
+                                    w[e] = e2m1::hmul2(w[e], *reinterpret_cast<const uint32_t*>(&a2));
+                                ptx::tmem_st16(s_addr + 16 * y, w);
+                            }
+                            if (c < 3) ptx::reg_fence<32>(buf[z ^ 1]);
                         }
-                    });
-                    m_tile = join_max(m4);
-                };
-                weights();
-                // seldom: a maximum more than 2^8 above the one used; the rows that
-                // have one take it, and the tile is done again
-                bool rescale = false;
-                float alpha = 1.f;
-                if (__any_sync(0xffffffffu, m_tile > m_used + kRescaleLog2)) {
-                    if (m_tile > m_used + kRescaleLog2) {
-                        alpha = ptx::ex2_approx(m_used - m_tile);
-                        m_used = m_tile;
-                        rescale = true;
+                        lsum = ptx::add2(lsum, ls[0]);
+                        ptx::tmem_st16(s_addr + 16 * c, pk);
                     }
-                    weights();
                 }
-                const float lsum = lsum0 + lsum1;
                 // tcgen05.ld/st are warp-collective: the whole warp rescales its
                 // rows when any row needs it (rows that do not use alpha = 1).
                 // PV of the previous tile has completed: S of this tile was issued
@@ -584,9 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                         ptx::tmem_st32(o_addr + 32 * c, o);
                     }
                 }
-                l = l * alpha + lsum;
-                ptx::tmem_st32(s_addr, pk);
-                ptx::tmem_st32(s_addr + 32, pk + 32);
+                l = l * alpha + (lsum.x + lsum.y);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
