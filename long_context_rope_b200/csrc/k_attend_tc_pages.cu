@@ -45,7 +45,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 512;
-constexpr float kMaxSum = 256.f;  // of 32 weights
+constexpr float kMaxSum = 8192.f;  // of a tile's weights
 constexpr int kSoftmaxRegs = 152, kControlRegs = 104, kTileRegs = 104;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kTileRegs <= 4 * 128,
               "the warpgroups share the registers of the launch, 128 a thread");
@@ -464,86 +464,82 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                 ptx::tc_fence_after();
                 const int blk0 = t * kBlocksPerTile;
                 const bool masked = sm.tile_last[bf][t] > tokx;
-                // Four chunks of 32 scores, the next one on its way while one is worked
-                // on: masked (causal within the current chunk, padding past the set),
-                // turned into P = 2^(S*sc - m) in fp16 and written over the scores of
-                // chunks already read. m is raised, to the chunk's maximum, only where
-                // a chunk's weights sum to more than 2^8 (seldom; without that no weight
-                // is above 2^8, far inside fp16) or there is no m yet; the row's weights
-                // and sum so far then shrink by alpha, and the chunk is done again. So
-                // no maximum is taken elsewhere.
-                float2 lsum = make_float2(0.f, 0.f);
+                // chunk c of 32 scores, masked: causal within the current chunk,
+                // padding past the set
+                auto mask = [&](int c, uint32_t (&s32)[32]) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int blk = blk0 + 2 * c + i;
+                        const int see = blk < nb ? qpos - sm.blk_pos[bf][blk] : -1;
+#pragma unroll
+                        for (int e = 0; e < kGroupRows; ++e)
+                            if (e > see) s32[16 * i + e] = __float_as_uint(-INFINITY);
+                    }
+                };
+                // P = 2^(S*sc - m) in fp16, the next chunk of scores on its way while one
+                // is worked on. m is the first tile's maximum; it is raised, to this
+                // tile's, only where the weights sum to more than kMaxSum (seldom;
+                // without that no weight is above it, far inside fp16). So no maximum
+                // is taken elsewhere. The sum so far then shrinks by alpha, and the
+                // tile's weights are made again.
+                uint32_t pk[kTileKeys / 2];
+                float2 lsum;
                 float alpha = 1.f;
                 bool rescale = false;
-                uint32_t buf[2][32];
-                ptx::tmem_ld32(s_addr, buf[0]);
+                for (bool raise = t == 0, last = false;;) {
+                    if (raise) {
+                        float mc = -INFINITY;
 #pragma unroll 1
-                for (int c0 = 0; c0 < 4; c0 += 2) {
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t s32[32];
+                            ptx::tmem_ld32(s_addr + 32 * c, s32);
+                            ptx::tmem_wait_ld();
+                            ptx::reg_fence<32>(s32);
+                            if (masked) mask(c, s32);
+                            float m4[4] = {mc, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int c = c0 + z;
-                        ptx::tmem_wait_ld();
-                        ptx::reg_fence<32>(buf[z]);
-                        if (c < 3) ptx::tmem_ld32(s_addr + 32 * (c + 1), buf[z ^ 1]);
-                        float* sx = reinterpret_cast<float*>(buf[z]);
-                        if (masked) {
+                            for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int blk = blk0 + 2 * c + i;
-                                const int see = blk < nb ? qpos - sm.blk_pos[bf][blk] : -1;
-#pragma unroll
-                                for (int e = 0; e < kGroupRows; ++e)
-                                    if (e > see) sx[16 * i + e] = -INFINITY;
-                            }
+                                for (int y = 0; y < 4; ++y)
+                                    m4[y] = ptx::fmax3(m4[y], __uint_as_float(s32[e + 2 * y]),
+                                                       __uint_as_float(s32[e + 2 * y + 1]));
+                            mc = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                         }
-                        uint32_t pk[16];
-                        float2 ls[2];
-                        for (bool again = false;; again = true) {
-                            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                            ls[0] = ls[1] = make_float2(0.f, 0.f);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float a0, a1;
-                                ptx::fma2_bc(sx[e], sx[e + 1], sc, neg_m, a0, a1);
-                                const float2 w =
-                                    make_float2(ptx::ex2_approx(a0), ptx::ex2_approx(a1));
-                                ls[(e >> 1) & 1] = ptx::add2(ls[(e >> 1) & 1], w);
-                                const __half2 h2 = __floats2half2_rn(w.x, w.y);
-                                pk[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-                            }
-                            ls[0] = ptx::add2(ls[0], ls[1]);
-                            const bool bad = ls[0].x + ls[0].y > kMaxSum || m_used == -INFINITY;
-                            if (again || !__any_sync(0xffffffffu, bad)) break;
-                            float mc = sx[0];
-#pragma unroll
-                            for (int e = 1; e < 32; ++e) mc = fmaxf(mc, sx[e]);
-                            mc *= sc;
-                            const bool above = bad && mc > m_used;
-                            // by a whole number, so that a is a power of two
-                            const float m_new =
-                                m_used == -INFINITY ? mc : m_used + ceilf(mc - m_used);
-                            const float a = above ? ptx::ex2_approx(m_used - m_new) : 1.f;
-                            m_used = above ? m_new : m_used;
-                            alpha *= a;
-                            lsum = ptx::mul2(lsum, make_float2(a, a));
-                            rescale = true;
-                            ptx::tmem_wait_st();
-                            for (int y = 0; y < c; ++y) {
-                                uint32_t w[16];
-                                ptx::tmem_ld16(s_addr + 16 * y, w);
-                                ptx::tmem_wait_ld();
-                                ptx::reg_fence<16>(w);
-                                const __half2 a2 = __float2half2_rn(a);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    w[e] = e2m1::hmul2(w[e], *reinterpret_cast<const uint32_t*>(&a2));
-                                ptx::tmem_st16(s_addr + 16 * y, w);
-                            }
-                            if (c < 3) ptx::reg_fence<32>(buf[z ^ 1]);
+                        const float m_new = fmaxf(m_used, mc * sc);
+                        if (m_new > m_used) {
+                            alpha = ptx::ex2_approx(m_used - m_new);
+                            m_used = m_new;
                         }
-                        lsum = ptx::add2(lsum, ls[0]);
-                        ptx::tmem_st16(s_addr + 16 * c, pk);
+                        rescale = true;
+                        last = t > 0;
                     }
+                    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t buf[2][32];
+                    ptx::tmem_ld32(s_addr, buf[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t(&s32)[32] = buf[c & 1];
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence<32>(s32);
+                        if (c < 3) ptx::tmem_ld32(s_addr + 32 * (c + 1), buf[(c + 1) & 1]);
+                        if (masked) mask(c, s32);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a0, a1;
+                            ptx::fma2_bc(__uint_as_float(s32[e]), __uint_as_float(s32[e + 1]), sc,
+                                         neg_m, a0, a1);
+                            const float2 w =
+                                make_float2(ptx::ex2_approx(a0), ptx::ex2_approx(a1));
+                            ls[(e >> 1) & 1] = ptx::add2(ls[(e >> 1) & 1], w);
+                            const __half2 h2 = __floats2half2_rn(w.x, w.y);
+                            pk[16 * c + e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                    }
+                    lsum = ptx::add2(ls[0], ls[1]);
+                    raise = lsum.x + lsum.y > kMaxSum || m_used == -INFINITY;
+                    if (last || !__any_sync(0xffffffffu, raise)) break;
+                    raise = true;
                 }
                 // tcgen05.ld/st are warp-collective: the whole warp rescales its
                 // rows when any row needs it (rows that do not use alpha = 1).
@@ -562,6 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                     }
                 }
                 l = l * alpha + (lsum.x + lsum.y);
+                ptx::tmem_st32(s_addr, pk);
+                ptx::tmem_st32(s_addr + 32, pk + 32);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
