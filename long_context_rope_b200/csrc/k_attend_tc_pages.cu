@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_pages_kernel(
                             m_used = m_new;
                         }
                         rescale = true;
-                        last = t > 0;
+                        last = true;  // NaN scores must not come back here
                     }
                     const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

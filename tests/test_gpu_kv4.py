@@ -240,6 +240,25 @@ def test_attend_nan_row(which, q_begin, q_len, heads):
         assert torch.isnan(out).all()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_begin,q_len,heads", [(199, 1, 8), (64, 140, 8), (150, 30, 3)])
+def test_attend_nan_query(value, q_begin, q_len, heads):
+    """A query with a NaN or an infinity makes its own row NaN, and no other."""
+    from long_context_rope_b200 import hga
+    cfg = _cfg4(hga, seq_len=256, q_begin=q_begin, q_len=q_len, n_q_heads=heads)
+    q, kp, vp, sel, n, want, tol = _attend_case(hga, cfg, 30)
+    t, h = q_len // 2, heads - 1
+    q[0, t, h, 5] = value
+    q[0, t, h, 6] = -value
+    out = torch.empty_like(q).cuda()
+    hga.attend(cfg, q.cuda(), kp.cuda(), vp.cuda(), sel.cuda(), n.cuda(), out)
+    _clean(hga)
+    got = out.cpu().double()
+    assert torch.isnan(got[0, t, h]).all()
+    got[0, t, h] = want[0, t, h]
+    _check(got, want, tol)
+
+
 @pytest.mark.parametrize("L", [1024, 999])
 @pytest.mark.parametrize("heads", [8, 5])
 def test_gathered_windows_and_warm(L, heads):
