@@ -81,31 +81,45 @@ __device__ __forceinline__ uint32_t select_nibbles(uint32_t a, uint32_t b) {
     return (a & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
 }
 
-// Sixteen elements of one block: their codes and the block's scale code, by
-// the rounding that hga_store_kv states. `ts` is the tensor scale. The divide
-// is the correctly rounded one: of bf16 elements and a power-of-two ts the
-// quotients that lie halfway between two codes are met exactly.
-__device__ __forceinline__ void quantise16(const float (&x)[kBlock], float ts, uint2& codes,
-                                           uint32_t& scale) {
-    float amax = 0.f;  // NaN if any element is
-#pragma unroll
-    for (int e = 0; e < kBlock; ++e)
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(x[e])));
-    codes = make_uint2(0u, 0u);
-    if (!(amax < INFINITY)) {
-        scale = 0x7fu;  // NaN: the block's values are NaN
-        return;
-    }
-    scale = scale_code(amax / (6.f * ts));
-    const float S = scale_value(scale) * ts;
-    if (!(S > 0.f)) {
-        scale = 0u;
-        return;
-    }
-    float q[kBlock];
-#pragma unroll
-    for (int e = 0; e < kBlock; ++e) q[e] = x[e] / S;
-    codes = make_uint2(f32x8_to_codes(q), f32x8_to_codes(q + 8));
+// Maximum that is NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// A block's scale by the rounding that hga_store_kv states: its code, S = its
+// value times the tensor scale, 1 / S. none: all codes 0 (a zero scale, or a
+// NaN or infinity in the block, whose scale is then NaN). slow: quotients by
+// an ordinary divide (saturated scales, whose quotients may be huge, and
+// magnitudes whose reciprocal or remainder could leave fp32's normal range).
+struct Scale {
+    uint32_t code;
+    float S, inv;
+    bool none, slow;
+};
+
+__device__ __forceinline__ Scale block_scale(float amax, float ts) {
+    Scale r;
+    const bool finite = amax < INFINITY;
+    r.code = finite ? scale_code(amax / (6.f * ts)) : 0x7fu;
+    r.S = scale_value(r.code) * ts;
+    r.none = !(r.S > 0.f);  // NaN too
+    if (r.none && finite) r.code = 0u;
+    r.slow = r.code == 0x7eu || r.S < 0x1p-80f || r.S > 0x1p80f;
+    r.inv = __frcp_rn(r.S);
+    return r;
+}
+
+// x / S, correctly rounded: the product with the rounded reciprocal, then
+// Markstein's correction by the exact remainder. Of bf16 elements and a
+// power-of-two tensor scale the quotients that lie halfway between two codes
+// are met exactly. (A divide per element made the store compute-bound.)
+__device__ __forceinline__ float quotient(float x, const Scale& s) {
+    if (s.none) return 0.f;
+    if (s.slow) return x / s.S;
+    const float q = x * s.inv;
+    return copysignf(fmaf(fmaf(-q, s.S, x), s.inv, q), x);
 }
 
 }  // namespace e2m1

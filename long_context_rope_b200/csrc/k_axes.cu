@@ -5,7 +5,10 @@
 // a = p[axis(i)] * theta_i, p the token's position on the pair's axis:
 //   y_i = x_i cos a - x_{i+d/2} sin a,   y_{i+d/2} = x_i sin a + x_{i+d/2} cos a.
 // The matrix is orthogonal, so the gradient of x is the rotation of y's by -a.
+#include <type_traits>
+
 #include "hga_kernels.h"
+#include "hga_turn.cuh"
 #include "hga_vec.cuh"
 
 namespace hga {
@@ -13,77 +16,95 @@ namespace hga {
 namespace {
 
 // ---------------------------------------------------------------- rotation
-// Memory-bound: x is read once and y written once with 16-byte accesses; the
-// angles cost a double product and reduction per (token, pair) and are the
-// same for every row (head) of a token, so a thread forms those of its V
-// pairs once and turns `rp` rows with them, kBatch rows' loads in flight.
-// Rows of a token: rr = r * n_heads + h, r < rep; thread groups of d/2/V lanes
-// take one token each. grid (tokens, sequences, row splits).
+// Memory-bound: x is read once and y written once with 16-byte accesses. The
+// angles, which every row (head) of a token shares, cost a double reduction
+// and two polynomials each: a CTA makes those of its `sites` (a site is one
+// token of one sequence) once, spread over its threads, and keeps cos and sin
+// in shared memory. Then a thread owns V pairs of one site in registers and
+// turns rows of it, kBatch rows' loads in flight. Rows of a site: rr = r *
+// n_heads + h, r < rep; thread (site, row lane, pair slice).
 constexpr int kRopeThreads = 256;
 constexpr int kBatch = 4;
+constexpr int kRopeAngles = kRopeThreads * 8;  // at most: sites x d/2
+
+struct RopeShape {
+    int64_t n_sites, n_tokens, rep;
+    int n_heads;
+    int lanes_log2;   // pair slices of a row: d/2 / V
+    int rlanes_log2;  // row lanes: rows that a site's threads turn at once
+    int rows_cta;     // rows per CTA (grid.y splits the rest)
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
-    Params p, AxisMap am, const int32_t* __restrict__ pos, const T* x, T* y, int64_t n_batch,
-    int64_t n_tokens, int n_heads, int64_t rep, int rp, int lanes_log2) {
+    const __grid_constant__ Params p, const __grid_constant__ AxisMap am, RopeShape sh,
+    const int32_t* __restrict__ pos, const T* x, T* y) {
     constexpr int V = Vec<T>::N;
-    const int half = p.d / 2;
-    const int64_t idx = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
-    const int64_t t = idx >> lanes_log2;
-    const int u = (int)(idx & ((1 << lanes_log2) - 1)) * V;
-    if (t >= n_tokens) return;
-    const int64_t rows = rep * n_heads;
-    for (int64_t nb = blockIdx.y; nb < n_batch; nb += gridDim.y) {
-        float c[V], s[V];
-        unsigned turn = 0;  // bit e: pair u + e is rotated
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int ax = am.axis[u + e];
-            c[e] = 1.f;
-            s[e] = 0.f;
-            if (ax >= 0) {
-                const int at = pos[((int64_t)ax * n_batch + nb) * n_tokens + t];
-                rope_cs((double)at, p.inv_freq[u + e], c[e], s[e]);
-                s[e] *= am.sign;
-                turn |= 1u << e;
-            }
+    __shared__ alignas(16) float s_c[kRopeAngles], s_s[kRopeAngles];
+    const int half = p.d / 2, tid = threadIdx.x;
+    const int sites_log2 = 8 - sh.lanes_log2 - sh.rlanes_log2;
+    const int64_t site0 = (int64_t)blockIdx.x << sites_log2;
+    {
+        // a thread makes one pair's angles only: the pair's axis and frequency are
+        // read once (their index differs from lane to lane, which the constant
+        // cache serves one lane at a time)
+        const int pair = tid & (half - 1), ax = am.axis[pair];
+        const double freq = p.inv_freq[pair];
+        for (int i = tid; i < half << sites_log2; i += kRopeThreads) {
+            const int64_t site = site0 + i / half;
+            float c = 1.f, sn = 0.f;
+            if (ax >= 0 && site < sh.n_sites) turn_cs((double)pos[ax * sh.n_sites + site], freq, c, sn);
+            s_c[i] = c;
+            s_s[i] = sn * am.sign;
         }
-        for (int64_t r0 = (int64_t)blockIdx.z * rp; r0 < rows; r0 += (int64_t)gridDim.z * rp) {
-            const int64_t r1 = r0 + rp < rows ? r0 + rp : rows;
-            int h = (int)(r0 % n_heads);
-            int64_t off = ((nb * rep + r0 / n_heads) * n_tokens + t) * n_heads + h;
-            for (int64_t rr = r0; rr < r1; rr += kBatch) {
-                int64_t o[kBatch];
-                typename Vec<T>::Raw ra[kBatch], rb[kBatch];
+    }
+    __syncthreads();
+    const int u = (tid & ((1 << sh.lanes_log2) - 1)) * V;
+    const int rl = (tid >> sh.lanes_log2) & ((1 << sh.rlanes_log2) - 1);
+    const int sl = tid >> (sh.lanes_log2 + sh.rlanes_log2);
+    const int64_t site = site0 + sl;
+    if (site >= sh.n_sites) return;
+    float c[V], s[V];
+    unsigned turn = 0;  // bit e: pair u + e is rotated
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    o[i] = off * p.d + u;
-                    if (rr + i < r1) {
-                        ra[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(x + o[i]);
-                        rb[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(x + o[i] + half);
-                    }
-                    ++off;
-                    if (++h == n_heads) {  // the same token of the sequence's next row
-                        h = 0;
-                        off += (n_tokens - 1) * n_heads;
-                    }
+    for (int e = 0; e < V; ++e) {
+        c[e] = s_c[sl * half + u + e];
+        s[e] = s_s[sl * half + u + e];
+        turn |= (am.axis[u + e] >= 0 ? 1u : 0u) << e;
+    }
+    const int64_t nb = site / sh.n_tokens, t = site % sh.n_tokens;
+    const int64_t rows = sh.rep * sh.n_heads;
+    const int step = 1 << sh.rlanes_log2;
+    for (int64_t z = blockIdx.y; z * sh.rows_cta < rows; z += gridDim.y) {
+        const int64_t r1 = (z + 1) * sh.rows_cta < rows ? (z + 1) * sh.rows_cta : rows;
+        for (int64_t rr = z * sh.rows_cta + rl; rr < r1; rr += (int64_t)step * kBatch) {
+            int64_t o[kBatch];
+            typename Vec<T>::Raw ra[kBatch], rb[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t ri = rr + (int64_t)i * step;
+                const int64_t r = sh.rep == 1 ? 0 : ri / sh.n_heads, h = ri - r * sh.n_heads;
+                o[i] = (((nb * sh.rep + r) * sh.n_tokens + t) * sh.n_heads + h) * p.d + u;
+                if (ri < r1) {
+                    ra[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(x + o[i]);
+                    rb[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(x + o[i] + half);
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    if (rr + i < r1) {
-                        float a[V], b[V], ya[V], yb[V];
-                        Vec<T>::unpack(ra[i], a);
-                        Vec<T>::unpack(rb[i], b);
+            for (int i = 0; i < kBatch; ++i) {
+                if (rr + (int64_t)i * step < r1) {
+                    float a[V], b[V], ya[V], yb[V];
+                    Vec<T>::unpack(ra[i], a);
+                    Vec<T>::unpack(rb[i], b);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            // an unrotated pair is copied, infinities among it
-                            const bool on = (turn >> e) & 1u;
-                            ya[e] = on ? a[e] * c[e] - b[e] * s[e] : a[e];
-                            yb[e] = on ? a[e] * s[e] + b[e] * c[e] : b[e];
-                        }
-                        Vec<T>::store(y + o[i], ya);
-                        Vec<T>::store(y + o[i] + half, yb);
+                    for (int e = 0; e < V; ++e) {
+                        // an unrotated pair is copied, infinities among it
+                        const bool on = (turn >> e) & 1u;
+                        ya[e] = on ? a[e] * c[e] - b[e] * s[e] : a[e];
+                        yb[e] = on ? a[e] * s[e] + b[e] * c[e] : b[e];
                     }
+                    Vec<T>::store(y + o[i], ya);
+                    Vec<T>::store(y + o[i] + half, yb);
                 }
             }
         }
@@ -91,142 +112,200 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
 }
 
 // --------------------------------------------------------------- summaries
-// One CTA per (sequence, KV head, chunk); thread (u, k, s) owns the V pairs
-// u*V .. of group k's tokens 16k + 4s + {0..3}. The chunk's positions and the
-// groups' and chunk's mean positions per axis sit in shared memory; sums of
-// integers, so the means are exact to double rounding.
-template <typename T, typename S>
-__global__ void summaries_axes_kernel(Params p, AxisMap am, const int32_t* __restrict__ pos,
-                                      const T* __restrict__ k_raw, S* __restrict__ cs,
-                                      S* __restrict__ gs, T* __restrict__ k_rot, int chunk_begin) {
-    constexpr int V = Vec<T>::N;
-    constexpr int kMaxRows = 8 * kGroupRows;  // groups_per_chunk <= 8
-    __shared__ int s_pos[HGA_MAX_AXES][kMaxRows];
-    __shared__ double s_mean[HGA_MAX_AXES][9];  // of groups 0..7, and of the chunk
-    const int half = p.d / 2;
-    const int G = p.G;
-    const int tid = threadIdx.x;
-    const int s = tid & 3;             // token lane within the group
-    const int k = (tid >> 2) % G;      // group within the chunk
-    const int u = tid / (4 * G);       // pair slice
+// One CTA per chunk, sequence and run of `hp` KV heads, which share the
+// chunk's angles: cos and sin of every token and pair, made once in shared
+// memory. Warp g owns group g: lane (q, u) the V pairs u*V .. of its tokens
+// q*R .. q*R + R - 1 (R = L/2 tokens for L lanes a row), so a warp's loads are
+// whole rows, and a group's sums need only shuffles over q. The chunk's sums go
+// over the groups in order. Mean positions are sums of integers, exact to
+// double rounding.
+//
+// In the tables, 16-byte piece j of a row sits at j ^ (j >> 3), so that the
+// eight lanes of a row read different banks.
+__device__ __forceinline__ int table_at(int row, int pair, int half) {
+    const int j = pair >> 2;
+    return row * half + ((j ^ (j >> 3)) << 2) + (pair & 3);
+}
+
+template <typename T, int D>
+struct SumShape {
+    static constexpr int V = Vec<T>::N, kHalf = D / 2;
+    static constexpr int L = kHalf / V;         // lanes of a row
+    static constexpr int R = kGroupRows * L / 32;  // tokens of a lane
+};
+
+template <typename T, typename S, int D>
+__global__ void __launch_bounds__(256) summaries_axes_kernel(
+    const __grid_constant__ Params p, const __grid_constant__ AxisMap am,
+    const int32_t* __restrict__ pos, const T* __restrict__ k_raw, S* __restrict__ cs,
+    S* __restrict__ gs, T* __restrict__ k_rot, int chunk_begin, int hp) {
+    using Sh = SumShape<T, D>;
+    constexpr int V = Sh::V, half = Sh::kHalf, L = Sh::L, R = Sh::R;
+    extern __shared__ __align__(16) float s_table[];      // cos of C x half, then sin
+    __shared__ int s_pos[HGA_MAX_AXES][8 * kGroupRows];   // groups_per_chunk <= 8
+    __shared__ int64_t s_psum[HGA_MAX_AXES][8];
+    __shared__ alignas(16) float s_mc[9][half], s_ms[9][half];  // mean angles: groups, chunk
+    __shared__ alignas(16) float s_sum[8][D];
+    const int G = p.G, tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
+    const int u = lane & (L - 1), q = lane / L;
     const int ch = chunk_begin + blockIdx.x;
-    const int64_t bh = blockIdx.y;
-    const int64_t b = bh / p.Hkv;
+    const int64_t b = blockIdx.y;
     const int64_t c0 = (int64_t)ch * p.C;
     const int n_rows = (int)(p.L - c0 < p.C ? p.L - c0 : p.C);  // >= 1
-    const T* base = k_raw + bh * (int64_t)p.L * p.d;
+    const int h0 = blockIdx.z * hp, h1 = h0 + hp < p.Hkv ? h0 + hp : p.Hkv;
+    const int row0 = kGroupRows * g + R * q;
+    float* tc = s_table;
+    float* ts = s_table + p.C * half;
 
-    typename Vec<T>::Raw raw_a[4], raw_b[4];
+    typename Vec<T>::Raw raw_a[R], raw_b[R];
+    auto load_rows = [&](int h) {
+        const T* base = k_raw + ((b * p.Hkv + h) * (int64_t)p.L + c0 + row0) * D + u * V;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int64_t t = c0 + 16 * k + 4 * s + m;
-        if (t < p.L) {
-            raw_a[m] = Vec<T>::load_raw(base + t * p.d + u * V);
-            raw_b[m] = Vec<T>::load_raw(base + t * p.d + half + u * V);
+        for (int m = 0; m < R; ++m) {
+            if (row0 + m < n_rows) {
+                raw_a[m] = Vec<T>::load_raw(base + m * D);
+                raw_b[m] = Vec<T>::load_raw(base + m * D + half);
+            }
+        }
+    };
+    load_rows(h0);
+    const int left = n_rows - kGroupRows * g;  // tokens of this group, if positive
+    const int n_g = left <= 0 ? 0 : (left >= kGroupRows ? kGroupRows : left);
+    for (int a = 0; a < am.n_axes; ++a) {
+        int64_t v = 0;
+        if (lane < n_g) {
+            const int at = pos[((int64_t)a * p.B + b) * p.L + c0 + kGroupRows * g + lane];
+            s_pos[a][kGroupRows * g + lane] = at;
+            v = at;
+        }
+#pragma unroll
+        for (int off = 1; off < kGroupRows; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) s_psum[a][g] = v;
+    }
+    __syncthreads();
+    {
+        // a thread makes one pair's angles at a time: the pair's axis and frequency
+        // are read once (their index differs from lane to lane, which the constant
+        // cache serves one lane at a time)
+        const int n_thr = 32 * G, per = n_thr >= half ? n_thr / half : 1;
+        const int stride = n_thr >= half ? per * half : n_thr;
+        if (tid < stride) {
+            for (int pair = tid % half; pair < half; pair += stride) {
+                const int ax = am.axis[pair];
+                const double freq = p.inv_freq[pair];
+                const bool low = pair >= p.F;
+                if (ax >= 0 && (!low || k_rot != nullptr))
+                    for (int r = tid / half; r < n_rows; r += per)
+                        turn_cs((double)s_pos[ax][r], freq, tc[table_at(r, pair, half)],
+                                ts[table_at(r, pair, half)]);
+                if (ax >= 0 && low)
+                    for (int i = tid / half; i <= G; i += per) {
+                        int64_t sum = 0;
+                        int n = n_rows;
+                        if (i < G) {
+                            sum = s_psum[ax][i];
+                            n = min(max(n_rows - kGroupRows * i, 1), kGroupRows);
+                        } else {
+                            for (int y = 0; y < G; ++y) sum += s_psum[ax][y];
+                        }
+                        turn_cs((double)sum / (double)n, freq, s_mc[i < G ? i : 8][pair],
+                                s_ms[i < G ? i : 8][pair]);
+                    }
+            }
         }
     }
-    for (int i = tid; i < am.n_axes * n_rows; i += blockDim.x) {
-        const int a = i / n_rows, r = i % n_rows;
-        s_pos[a][r] = pos[((int64_t)a * p.B + b) * p.L + c0 + r];
-    }
-    __syncthreads();
-    for (int i = tid; i < am.n_axes * (G + 1); i += blockDim.x) {
-        const int a = i / (G + 1), g = i % (G + 1);
-        const int lo = g < G ? 16 * g : 0;
-        const int hi = g < G && 16 * g + 16 < n_rows ? 16 * g + 16 : n_rows;
-        int64_t sum = 0;
-        for (int r = lo; r < hi; ++r) sum += s_pos[a][r];
-        s_mean[a][g < G ? g : 8] = hi > lo ? (double)sum / (double)(hi - lo) : 0.0;
+    // bit e: pair u*V + e is rotated; token by token in the sums; by the mean angle
+    unsigned turn = 0, each = 0, mean = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const bool on = am.axis[u * V + e] >= 0, low = u * V + e >= p.F;
+        turn |= (on && (!low || k_rot != nullptr) ? 1u : 0u) << e;
+        each |= (on && !low ? 1u : 0u) << e;
+        mean |= (on && low ? 1u : 0u) << e;
     }
     __syncthreads();
 
-    float acc0[V], acc1[V];
-    int ax[V];
+    for (int h = h0; h < h1; ++h) {
+        const int64_t bh = b * p.Hkv + h;
+        float acc0[V], acc1[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        acc0[e] = acc1[e] = 0.f;
-        ax[e] = am.axis[u * V + e];
-    }
+        for (int e = 0; e < V; ++e) acc0[e] = acc1[e] = 0.f;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int r = 16 * k + 4 * s + m;
-        if (r < n_rows) {
-            float a[V], bb[V], ra[V], rb[V];
-            Vec<T>::unpack(raw_a[m], a);
-            Vec<T>::unpack(raw_b[m], bb);
+        for (int m = 0; m < R; ++m) {
+            const int r = row0 + m;
+            if (r < n_rows) {
+                float a[V], bb[V], c[V], sn[V];
+                Vec<T>::unpack(raw_a[m], a);
+                Vec<T>::unpack(raw_b[m], bb);
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    const int at = table_at(r, u * V + e, half);
+                    *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(tc + at);
+                    *reinterpret_cast<float4*>(sn + e) = *reinterpret_cast<const float4*>(ts + at);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const bool on = (turn >> e) & 1u, in = (each >> e) & 1u;
+                    const float ra = on ? a[e] * c[e] - bb[e] * sn[e] : a[e];
+                    const float rb = on ? a[e] * sn[e] + bb[e] * c[e] : bb[e];
+                    acc0[e] += in ? ra : a[e];
+                    acc1[e] += in ? rb : bb[e];
+                    a[e] = ra;
+                    bb[e] = rb;
+                }
+                if (k_rot != nullptr) {
+                    T* orow = k_rot + (bh * (int64_t)p.L + c0 + r) * D + u * V;
+                    Vec<T>::store(orow, a);
+                    Vec<T>::store(orow + half, bb);
+                }
+            }
+        }
+        if (h + 1 < h1) load_rows(h + 1);  // in flight over the reductions
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int off = L; off < 32; off <<= 1) {
+                acc0[e] += __shfl_xor_sync(0xffffffffu, acc0[e], off);
+                acc1[e] += __shfl_xor_sync(0xffffffffu, acc1[e], off);
+            }
+        }
+        auto finish = [&](const float* s0, const float* s1, int i, int n, S* out) {
+            float o0[V], o1[V];
+            const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const int i = u * V + e;
-                ra[e] = a[e];
-                rb[e] = bb[e];
-                if (ax[e] >= 0 && (i < p.F || k_rot != nullptr)) {
-                    float c, sn;
-                    rope_cs((double)s_pos[ax[e]][r], p.inv_freq[i], c, sn);
-                    ra[e] = a[e] * c - bb[e] * sn;
-                    rb[e] = a[e] * sn + bb[e] * c;
+                const float m0 = s0[e] * inv_n, m1 = s1[e] * inv_n;
+                const float c = s_mc[i][u * V + e], sn = s_ms[i][u * V + e];
+                const bool on = n > 0 && ((mean >> e) & 1u);
+                o0[e] = on ? m0 * c - m1 * sn : m0;
+                o1[e] = on ? m0 * sn + m1 * c : m1;
+            }
+            store_sum(out + u * V, o0, V);
+            store_sum(out + half + u * V, o1, V);
+        };
+        if (q == 0) {
+            finish(acc0, acc1, g, n_g, gs + ((bh * p.nC + ch) * G + g) * (int64_t)D);
+#pragma unroll
+            for (int e = 0; e < V; e += 4) {
+                *reinterpret_cast<float4*>(&s_sum[g][u * V + e]) =
+                    *reinterpret_cast<const float4*>(acc0 + e);
+                *reinterpret_cast<float4*>(&s_sum[g][half + u * V + e]) =
+                    *reinterpret_cast<const float4*>(acc1 + e);
+            }
+        }
+        __syncthreads();
+        if (tid < L) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                acc0[e] = acc1[e] = 0.f;
+                for (int y = 0; y < G; ++y) {
+                    acc0[e] += s_sum[y][u * V + e];
+                    acc1[e] += s_sum[y][half + u * V + e];
                 }
-                acc0[e] += i < p.F ? ra[e] : a[e];
-                acc1[e] += i < p.F ? rb[e] : bb[e];
             }
-            if (k_rot != nullptr) {
-                T* orow = k_rot + (bh * (int64_t)p.L + c0 + r) * p.d;
-                Vec<T>::store(orow + u * V, ra);
-                Vec<T>::store(orow + half + u * V, rb);
-            }
+            finish(acc0, acc1, 8, n_rows, cs + (bh * p.nC + ch) * (int64_t)D);
         }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-#pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-            acc0[e] += __shfl_xor_sync(0xffffffffu, acc0[e], off);
-            acc1[e] += __shfl_xor_sync(0xffffffffu, acc1[e], off);
-        }
-    }
-    auto finish = [&](const float* s0, const float* s1, int g, int n, S* out) {
-        float o0[V], o1[V];
-        const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int i = u * V + e;
-            const float m0 = s0[e] * inv_n, m1 = s1[e] * inv_n;
-            o0[e] = m0;
-            o1[e] = m1;
-            if (n > 0 && i >= p.F && ax[e] >= 0) {
-                float c, sn;
-                rope_cs(s_mean[ax[e]][g], p.inv_freq[i], c, sn);
-                o0[e] = m0 * c - m1 * sn;
-                o1[e] = m0 * sn + m1 * c;
-            }
-        }
-        store_sum(out + u * V, o0, V);
-        store_sum(out + half + u * V, o1, V);
-    };
-    if (s == 0) {
-        const int left = n_rows - 16 * k;
-        finish(acc0, acc1, k, left <= 0 ? 0 : (left >= 16 ? 16 : left),
-               gs + ((bh * p.nC + ch) * G + k) * (int64_t)p.d);
-    }
-    // chunk sums over the groups, in group order (G need not be a power of two)
-    __shared__ float s_sum[8][128];
-    if (s == 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            s_sum[k][u * V + e] = acc0[e];
-            s_sum[k][half + u * V + e] = acc1[e];
-        }
-    }
-    __syncthreads();
-    if (s == 0 && k == 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            acc0[e] = acc1[e] = 0.f;
-            for (int g = 0; g < G; ++g) {
-                acc0[e] += s_sum[g][u * V + e];
-                acc1[e] += s_sum[g][half + u * V + e];
-            }
-        }
-        finish(acc0, acc1, 8, n_rows, cs + (bh * p.nC + ch) * (int64_t)p.d);
+        __syncthreads();
     }
 }
 
@@ -237,28 +316,37 @@ cudaError_t launch_rope_axes(const Params& p, const AxisMap& am, const int32_t* 
                              int64_t n_tokens, int n_heads, cudaStream_t st) {
     const int V = p.dtype == HGA_BF16 ? 8 : 4;
     const int lanes = p.d / 2 / V;
-    int lanes_log2 = 0;
-    while ((1 << lanes_log2) < lanes) ++lanes_log2;
-    const int64_t rep = n_outer / n_batch, rows = rep * n_heads;
-    // rows per thread: one while the call is small (latency), more once the
-    // threads fill the GPU about four times over (the angles' cost is shared)
-    const int64_t threads = n_batch * n_tokens * rows * lanes;
-    int rp = 1;
-    while (rp < 16 && threads / (2 * rp) >= (int64_t)148 * 2048 * 4) rp *= 2;
-    const int64_t bx = (n_tokens * lanes + kRopeThreads - 1) / kRopeThreads;
-    const int64_t bz = (rows + rp - 1) / rp;
+    RopeShape sh;
+    sh.n_sites = n_batch * n_tokens;
+    sh.n_tokens = n_tokens;
+    sh.rep = n_outer / n_batch;
+    sh.n_heads = n_heads;
+    sh.lanes_log2 = sh.rlanes_log2 = 0;
+    while ((1 << sh.lanes_log2) < lanes) ++sh.lanes_log2;
+    const int64_t rows = sh.rep * n_heads;
+    // Row lanes: 8 where there are that many rows, more only while there are
+    // fewer sites than a CTA would then take.
+    while (sh.lanes_log2 + sh.rlanes_log2 < 8 && (2 << sh.rlanes_log2) <= rows &&
+           (sh.rlanes_log2 < 3 || (1 << (8 - sh.lanes_log2 - sh.rlanes_log2)) > sh.n_sites))
+        ++sh.rlanes_log2;
+    const int sites_log2 = 8 - sh.lanes_log2 - sh.rlanes_log2;
+    const int64_t bx = (sh.n_sites + (1 << sites_log2) - 1) >> sites_log2;
+    // Rows per CTA: one batch while the grid is short of two CTAs per SM (the
+    // angles are made again, the call's latency counts), more up to all of a
+    // site's rows once it fills the GPU.
+    int64_t per = (int64_t)1 << sh.rlanes_log2;
+    while (per < rows && bx * ((rows + per - 1) / per) > 2 * 148) per *= 2;
+    sh.rows_cta = (int)(per < (1 << 20) ? per : (1 << 20));
+    const int64_t by = (rows + sh.rows_cta - 1) / sh.rows_cta;
     if (bx > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)bx, (unsigned)(n_batch < 65535 ? n_batch : 65535),
-                    (unsigned)(bz < 65535 ? bz : 65535));
+    const dim3 grid((unsigned)bx, (unsigned)(by < 65535 ? by : 65535));
     using bf = __nv_bfloat16;
     if (p.dtype == HGA_BF16)
-        rope_axes_kernel<bf><<<grid, kRopeThreads, 0, st>>>(p, am, positions, (const bf*)x, (bf*)y,
-                                                            n_batch, n_tokens, n_heads, rep, rp,
-                                                            lanes_log2);
+        rope_axes_kernel<bf><<<grid, kRopeThreads, 0, st>>>(p, am, sh, positions, (const bf*)x,
+                                                            (bf*)y);
     else
-        rope_axes_kernel<float><<<grid, kRopeThreads, 0, st>>>(
-            p, am, positions, (const float*)x, (float*)y, n_batch, n_tokens, n_heads, rep, rp,
-            lanes_log2);
+        rope_axes_kernel<float><<<grid, kRopeThreads, 0, st>>>(p, am, sh, positions,
+                                                               (const float*)x, (float*)y);
     return cudaGetLastError();
 }
 
@@ -266,21 +354,33 @@ cudaError_t launch_summaries_axes(const Params& p, const AxisMap& am, const int3
                                   const void* k_raw, void* chunk_sum, void* group_sum,
                                   void* k_rot, int chunk_begin, int chunk_end, cudaStream_t st) {
     using bf = __nv_bfloat16;
-    const int V = p.dtype == HGA_BF16 ? 8 : 4;
-    const int threads = (p.d / 2 / V) * 4 * p.G;
-    const dim3 grid(chunk_end - chunk_begin, p.B * p.Hkv);
-    auto run = [&](auto t, auto s) {
+    // heads per CTA: all of them, halved while the grid is short of four CTAs per SM
+    int hp = p.Hkv;
+    auto ctas = [&](int n) {
+        return (int64_t)(chunk_end - chunk_begin) * p.B * ((p.Hkv + n - 1) / n);
+    };
+    while (hp > 1 && ctas(hp) < 4 * 148) hp = (hp + 1) / 2;
+    const int groups = (p.Hkv + hp - 1) / hp;
+    if (p.B > 65535 || groups > 65535) return cudaErrorInvalidValue;
+    const dim3 grid(chunk_end - chunk_begin, p.B, groups);
+    const size_t smem = (size_t)p.C * p.d * sizeof(float);
+    auto run = [&](auto t, auto s, auto d) {
         using T = decltype(t);
         using S = decltype(s);
-        summaries_axes_kernel<T, S><<<grid, threads, 0, st>>>(
-            p, am, positions, (const T*)k_raw, (S*)chunk_sum, (S*)group_sum, (T*)k_rot, chunk_begin);
+        auto* kernel = summaries_axes_kernel<T, S, decltype(d)::value>;
+        const cudaError_t e = set_func_attr_once(
+            (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 128 * 4);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, 32 * p.G, smem, st>>>(p, am, positions, (const T*)k_raw, (S*)chunk_sum,
+                                            (S*)group_sum, (T*)k_rot, chunk_begin, hp);
+        return cudaGetLastError();
     };
-    if (p.dtype == HGA_BF16) {
-        if (p.sum_bf16) run(bf(), bf()); else run(bf(), float());
-    } else {
-        if (p.sum_bf16) run(float(), bf()); else run(float(), float());
-    }
-    return cudaGetLastError();
+    auto by_dim = [&](auto t, auto s) {
+        return p.d == 128 ? run(t, s, std::integral_constant<int, 128>())
+                          : run(t, s, std::integral_constant<int, 64>());
+    };
+    if (p.dtype == HGA_BF16) return p.sum_bf16 ? by_dim(bf(), bf()) : by_dim(bf(), float());
+    return p.sum_bf16 ? by_dim(float(), bf()) : by_dim(float(), float());
 }
 
 }  // namespace hga

@@ -4,116 +4,213 @@
 // scale is the E4M3 number nearest amax / (6 * tensor scale) and its codes
 // the E2M1 numbers nearest x / (scale * tensor scale). Keys may be rotated
 // on the way, in 64 bits and rounded once to fp32: an error of the angle near
-// a border between two codes would move the stored value by a third. hga_load_kv: code * scale (exact in f16) * tensor scale, rounded
-// once to bf16. Both are memory-bound: 256 bytes of bf16 against 72 of the
-// store per row and tensor.
+// a border between two codes would move the stored value by a third.
+// hga_load_kv: code * scale (exact in f16) * tensor scale, rounded once to
+// bf16. Both are memory-bound (256 bytes of bf16 against 72 of the store per
+// row and tensor), so what counts is that every access of a warp covers whole
+// sectors, with a few loads in flight per thread, and few instructions per
+// element (a correctly rounded quotient in three).
 #include "hga_e2m1.cuh"
 #include "hga_kernels.h"
+#include "hga_turn.cuh"
 
 namespace hga {
 
 namespace {
 
+using e2m1::kBlock;
+using bf = __nv_bfloat16;
+
 constexpr int kStoreThreads = 256;
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* x, float* f) {
-    const uint4 a = *reinterpret_cast<const uint4*>(x);
-    const uint4 b = *reinterpret_cast<const uint4*>(x + 8);
-    bf16x8_to_f32(a, f);
-    bf16x8_to_f32(b, f + 8);
+// Where token `at` of unit bh starts in a store: its page; *row: within it.
+__device__ __forceinline__ int64_t page_of(const Params& p, int64_t bh, int64_t at, int* row) {
+    *row = (int)(at % kGroupRows);
+    return bh * p.kv_slab + (at / kGroupRows) * kE2m1Page;
 }
 
-// Thread (row, s): blocks s and s + 4 of the row's key, then of its value
-// (dims 16s.. and 64 + 16s.., the two halves of the same rotary pairs).
-__global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(
-    Params p, AxisMap am, const int32_t* __restrict__ pos, const __nv_bfloat16* __restrict__ k,
-    const __nv_bfloat16* __restrict__ v, uint8_t* __restrict__ ks, uint8_t* __restrict__ vs,
-    int64_t pos0, int64_t n_tokens, int64_t n_rows) {
-    for (int64_t it = (int64_t)blockIdx.x * kStoreThreads + threadIdx.x; it < n_rows * 4;
-         it += (int64_t)gridDim.x * kStoreThreads) {
-        const int s = (int)(it & 3);
-        const int64_t row = it >> 2, bh = row / n_tokens, t = row % n_tokens;
-        const int64_t at = pos0 + t;
-        const int64_t page = bh * p.kv_slab + (at / kGroupRows) * kE2m1Page;
-        const int pr = (int)(at % kGroupRows);
-        float a[16], b[16];
-        load16(k + row * 128 + 16 * s, a);
-        load16(k + row * 128 + 64 + 16 * s, b);
-        if (am.n_axes > 0) {
+// Rows as they are. Item = (row, block): row * 8 + block, so eight lanes hold
+// the eight blocks of a row; its scales are written four bytes at a time. I: an
+// unsigned type that holds the item count and a grid more.
+template <typename I>
+__device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8_t* store, float ts,
+                                           int64_t pos0, I n_tokens, I n_rows) {
+    const int blk = threadIdx.x & 7;
+    const I n_items = n_rows * 8;
+    // whole warps stay to the end: their lanes exchange scales
+    for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; (it & ~(I)31) < n_items;
+         it += (I)gridDim.x * kStoreThreads) {
+        const bool ok = it < n_items;
+        const I row = ok ? it >> 3 : 0, bh = row / n_tokens, t = row - bh * n_tokens;
+        const uint4* src16 = reinterpret_cast<const uint4*>(src + (int64_t)row * 128 + kBlock * blk);
+        const uint4 r0 = src16[0], r1 = src16[1];
+        const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+        // the largest magnitude as bits; infinities and NaN are the largest
+        uint32_t m = 0u;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int i = 16 * s + e, ax = am.axis[i];
-                if (ax >= 0) {
-                    const double x =
-                        pos ? (double)pos[((int64_t)ax * p.B + bh / p.Hkv) * n_tokens + t] : (double)at;
-                    double c, sn;
-                    sincos(x * p.inv_freq[i], &sn, &c);
-                    const double ra = (double)a[e] * c - (double)b[e] * sn;
-                    b[e] = (float)((double)a[e] * sn + (double)b[e] * c);
-                    a[e] = (float)ra;
-                }
-            }
-        }
-        auto put = [&](uint8_t* store, float ts) {
-            uint2 c0, c1;
-            uint32_t s0, s1;
-            e2m1::quantise16(a, ts, c0, s0);
-            e2m1::quantise16(b, ts, c1, s1);
-            uint8_t* pg = store + page;
-            *reinterpret_cast<uint2*>(pg + e2m1::code_at(pr, 16 * s)) = c0;
-            *reinterpret_cast<uint2*>(pg + e2m1::code_at(pr, 64 + 16 * s)) = c1;
-            pg[e2m1::scale_at(pr, s)] = (uint8_t)s0;
-            pg[e2m1::scale_at(pr, s + 4)] = (uint8_t)s1;
-        };
-        put(ks, p.k_scale);
-        load16(v + row * 128 + 16 * s, a);
-        load16(v + row * 128 + 64 + 16 * s, b);
-        put(vs, p.v_scale);
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        m = max(m >> 16, m & 0xffffu);
+        const e2m1::Scale sc = e2m1::block_scale(__uint_as_float(m << 16), ts);
+        float x[kBlock];
+        bf16x8_to_f32(r0, x);
+        bf16x8_to_f32(r1, x + 8);
+#pragma unroll
+        for (int e = 0; e < kBlock; ++e) x[e] = e2m1::quotient(x[e], sc);
+        int pr;
+        uint8_t* pg = store + page_of(p, bh, pos0 + t, &pr);
+        if (ok)
+            *reinterpret_cast<uint2*>(pg + e2m1::code_at(pr, kBlock * blk)) =
+                make_uint2(e2m1::f32x8_to_codes(x), e2m1::f32x8_to_codes(x + 8));
+        uint32_t four = sc.code << (8 * (blk & 3));
+        four |= __shfl_xor_sync(0xffffffffu, four, 1);
+        four |= __shfl_xor_sync(0xffffffffu, four, 2);
+        if (ok && (blk & 3) == 0) *reinterpret_cast<uint32_t*>(pg + e2m1::scale_at(pr, blk)) = four;
     }
 }
 
-// Thread (row, tile): 32 dims of the key, then of the value.
+// Keys rotated on the way. 16 lanes a row, each with 4 rotary pairs: dims
+// 4l .. + 3 and 64 + 4l .. + 3. Item = (row, lane): row * 16 + lane.
+template <typename I>
+__device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am,
+                                              const int32_t* pos, const bf* k, uint8_t* ks,
+                                              int64_t pos0, I n_tokens, I n_rows) {
+    const int l = threadIdx.x & 15;
+    const I n_items = n_rows * 16;
+    // this lane's pairs, read once (the constant cache serves one index at a time)
+    double freq[4];
+    int axis[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        freq[e] = p.inv_freq[4 * l + e];
+        axis[e] = am.axis[4 * l + e];
+    }
+    for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; (it & ~(I)31) < n_items;
+         it += (I)gridDim.x * kStoreThreads) {
+        const bool ok = it < n_items;
+        const I row = ok ? it >> 4 : 0, bh = row / n_tokens, t = row - bh * n_tokens;
+        const int64_t at = pos0 + t;
+        const uint2* src8 = reinterpret_cast<const uint2*>(k + (int64_t)row * 128 + 4 * l);
+        const uint2 lo = src8[0], hi = src8[16];
+        const uint32_t wl[2] = {lo.x, lo.y}, wh[2] = {hi.x, hi.y};
+        float x[2][4];  // dims 4l .. and 64 + 4l ..
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = __uint_as_float((e & 1) ? wl[e >> 1] & 0xffff0000u : wl[e >> 1] << 16);
+            const float b = __uint_as_float((e & 1) ? wh[e >> 1] & 0xffff0000u : wh[e >> 1] << 16);
+            x[0][e] = a;
+            x[1][e] = b;
+            if (axis[e] >= 0) {
+                const double at_axis =
+                    pos ? (double)pos[((int64_t)axis[e] * p.B + bh / p.Hkv) * n_tokens + t] : (double)at;
+                double c, sn;
+                turn_cs64(at_axis, freq[e], c, sn);
+                x[0][e] = (float)((double)a * c - (double)b * sn);
+                x[1][e] = (float)((double)a * sn + (double)b * c);
+            }
+        }
+        int pr;
+        uint8_t* pg = ks + page_of(p, bh, at, &pr);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            float amax = 0.f;  // NaN if any element of the block is
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = e2m1::max_nan(amax, fabsf(x[y][e]));
+            amax = e2m1::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = e2m1::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const e2m1::Scale sc = e2m1::block_scale(amax, p.k_scale);
+            float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = e2m1::quotient(x[y][e], sc);
+            const uint32_t w = e2m1::f32x8_to_codes(q) & 0xffffu;
+            // four lanes' 16 bits of codes to the first of them
+            const uint32_t w1 = w | (__shfl_down_sync(0xffffffffu, w, 1) << 16);
+            const uint32_t w2 = __shfl_down_sync(0xffffffffu, w1, 2);
+            const int blk = 4 * y + (l >> 2);
+            if (ok && (l & 3) == 0) {
+                *reinterpret_cast<uint2*>(pg + e2m1::code_at(pr, kBlock * blk)) = make_uint2(w1, w2);
+                pg[e2m1::scale_at(pr, blk)] = (uint8_t)sc.code;
+            }
+        }
+    }
+}
+
+// grid.y = 0: keys, 1: values.
+template <typename I, bool kRotate>
+__global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(
+    const __grid_constant__ Params p, const __grid_constant__ AxisMap am,
+    const int32_t* __restrict__ pos, const bf* __restrict__ k, const bf* __restrict__ v,
+    uint8_t* __restrict__ ks, uint8_t* __restrict__ vs, int64_t pos0, I n_tokens, I n_rows) {
+    if (blockIdx.y == 1)
+        store_rows<I>(p, v, vs, p.v_scale, pos0, n_tokens, n_rows);
+    else if (kRotate)
+        store_rotated<I>(p, am, pos, k, ks, pos0, n_tokens, n_rows);
+    else
+        store_rows<I>(p, k, ks, p.k_scale, pos0, n_tokens, n_rows);
+}
+
+// grid.y = 0: keys, 1: values. Item = (row, 8 dims): row * 16 + piece; a
+// thread has kLoadItems of them in flight, a grid apart.
+constexpr int kLoadItems = 4;
+
+template <typename I>
 __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
-    Params p, const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
-    __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v, int64_t pos0, int64_t n_tokens,
-    int64_t n_rows) {
-    for (int64_t it = (int64_t)blockIdx.x * kStoreThreads + threadIdx.x; it < n_rows * 4;
-         it += (int64_t)gridDim.x * kStoreThreads) {
-        const int tile = (int)(it & 3);
-        const int64_t row = it >> 2, bh = row / n_tokens, at = pos0 + row % n_tokens;
-        const int64_t page = bh * p.kv_slab + (at / kGroupRows) * kE2m1Page;
-        const int pr = (int)(at % kGroupRows);
+    const __grid_constant__ Params p, const uint8_t* __restrict__ ks,
+    const uint8_t* __restrict__ vs, bf* __restrict__ k, bf* __restrict__ v, int64_t pos0,
+    I n_tokens, I n_items) {
+    const uint8_t* store = blockIdx.y ? vs : ks;
+    bf* dst = blockIdx.y ? v : k;
+    const float ts = blockIdx.y ? p.v_scale : p.k_scale;
+    const int pc = threadIdx.x & 15;
+    const I step = (I)gridDim.x * kStoreThreads;
+    for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; it < n_items; it += step * kLoadItems) {
+        uint32_t w[kLoadItems];
+        uint8_t sc[kLoadItems];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const uint8_t* pg = (x ? vs : ks) + page;
-            const float ts = x ? p.v_scale : p.k_scale;
-            __nv_bfloat16* out = (x ? v : k) + row * 128 + 32 * tile;
-            const uint4 c = *reinterpret_cast<const uint4*>(pg + e2m1::code_at(pr, 32 * tile));
-            const uint16_t s2 = *reinterpret_cast<const uint16_t*>(pg + e2m1::scale_at(pr, 2 * tile));
-            const uint32_t sc = e2m1::scales_to_f16x2(s2);
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        for (int i = 0; i < kLoadItems; ++i) {
+            const I x = it + step * i;
+            if (x < n_items) {
+                const I row = x >> 4, bh = row / n_tokens, t = row - bh * n_tokens;
+                int pr;
+                const uint8_t* pg = store + page_of(p, bh, pos0 + t, &pr);
+                w[i] = *reinterpret_cast<const uint32_t*>(pg + e2m1::code_at(pr, 8 * pc));
+                sc[i] = pg[e2m1::scale_at(pr, pc >> 1)];
+            }
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t sd = i < 2 ? __byte_perm(sc, 0, 0x1010) : __byte_perm(sc, 0, 0x3232);
+        for (int i = 0; i < kLoadItems; ++i) {
+            const I x = it + step * i;
+            if (x < n_items) {
+                const uint32_t s2 = e2m1::scales_to_f16x2((uint16_t)(sc[i] * 0x101u));
                 uint32_t f[4];
                 e2m1::codes_to_f16x2(w[i], f);
                 float o[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t h = e2m1::hmul2(f[e], sd);
+                    const uint32_t h = e2m1::hmul2(f[e], s2);
                     const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h));
                     o[2 * e] = r.x * ts;
                     o[2 * e + 1] = r.y * ts;
                 }
-                *reinterpret_cast<uint4*>(out + 8 * i) = f32x8_to_bf16(o);
+                *reinterpret_cast<uint4*>(dst + (int64_t)(x >> 4) * 128 + 8 * pc) = f32x8_to_bf16(o);
             }
         }
     }
 }
 
-unsigned grid_of(int64_t n_rows) {
-    const int64_t blocks = (n_rows * 4 + kStoreThreads - 1) / kStoreThreads;
-    return (unsigned)(blocks < 148 * 64 ? blocks : 148 * 64);
+// CTAs for `items` threads, at most 16 an SM.
+unsigned grid_of(int64_t items) {
+    const int64_t blocks = (items + kStoreThreads - 1) / kStoreThreads;
+    return (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16);
+}
+
+// f(an unsigned item type): 32 bits where items and the grids' strides past
+// them fit.
+template <typename F>
+void with_index(int64_t items, F f) {
+    if (items < (int64_t)1 << 30)
+        f(uint32_t());
+    else
+        f(uint64_t());
 }
 
 }  // namespace
@@ -121,20 +218,33 @@ unsigned grid_of(int64_t n_rows) {
 cudaError_t launch_store_kv(const Params& p, const AxisMap& am, const int32_t* positions,
                             const void* k, const void* v, void* k_store, void* v_store,
                             int64_t pos0, int64_t n_tokens, cudaStream_t st) {
-    using bf = __nv_bfloat16;
     const int64_t rows = (int64_t)p.B * p.Hkv * n_tokens;
-    store_kv_kernel<<<grid_of(rows), kStoreThreads, 0, st>>>(
-        p, am, positions, (const bf*)k, (const bf*)v, (uint8_t*)k_store, (uint8_t*)v_store, pos0,
-        n_tokens, rows);
+    const bool rotate = am.n_axes > 0;
+    with_index(rows * 16, [&](auto i) {
+        using I = decltype(i);
+        auto run = [&](auto* kernel, int lanes) {
+            kernel<<<dim3(grid_of(rows * lanes), 2), kStoreThreads, 0, st>>>(
+                p, am, positions, (const bf*)k, (const bf*)v, (uint8_t*)k_store, (uint8_t*)v_store,
+                pos0, (I)n_tokens, (I)rows);
+        };
+        if (rotate)
+            run(store_kv_kernel<I, true>, 16);
+        else
+            run(store_kv_kernel<I, false>, 8);
+    });
     return cudaGetLastError();
 }
 
 cudaError_t launch_load_kv(const Params& p, const void* k_store, const void* v_store, void* k,
                            void* v, int64_t pos0, int64_t n_tokens, cudaStream_t st) {
-    using bf = __nv_bfloat16;
     const int64_t rows = (int64_t)p.B * p.Hkv * n_tokens;
-    load_kv_kernel<<<grid_of(rows), kStoreThreads, 0, st>>>(
-        p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, pos0, n_tokens, rows);
+    with_index(rows * 16, [&](auto i) {
+        using I = decltype(i);
+        const dim3 grid(grid_of((rows * 16 + kLoadItems - 1) / kLoadItems), 2);
+        load_kv_kernel<I><<<grid, kStoreThreads, 0, st>>>(
+            p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, pos0, (I)n_tokens,
+            (I)(rows * 16));
+    });
     return cudaGetLastError();
 }
 

@@ -202,7 +202,8 @@ def config_from(w, **overrides) -> HgaConfig:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without its Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -218,9 +219,12 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=Tr
         raise TypeError(f"{name} must be a torch.Tensor")
     if device and not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if device and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device, cuda:{torch._C._cuda_getDevice()}, "
+                         f"not on {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
