@@ -25,18 +25,56 @@ namespace {
 // n_heads + h, r < rep; thread (site, row lane, pair slice).
 constexpr int kRopeThreads = 256;
 constexpr int kBatch = 4;
+constexpr int kRopeCtas = 3;
 constexpr int kRopeAngles = kRopeThreads * 8;  // at most: sites x d/2
+
+constexpr float kNoTurn = 2.f;  // in place of the cosine of a pair on no axis
+
+// A row's V pairs (a_e, b_e) turned in place, a few elements at a time to keep
+// registers few. kAll: every pair is rotated; else those on no axis are copied,
+// infinities among them.
+template <bool kAll>
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+    const float ya = a * c - b * s, yb = a * s + b * c;
+    a = kAll || c != kNoTurn ? ya : a;
+    b = kAll || c != kNoTurn ? yb : b;
+}
+template <typename T, bool kAll>
+__device__ __forceinline__ void turn_row(float4& a, float4& b, const float* c, const float* s) {
+    turn_pair<kAll>(a.x, b.x, c[0], s[0]);
+    turn_pair<kAll>(a.y, b.y, c[1], s[1]);
+    turn_pair<kAll>(a.z, b.z, c[2], s[2]);
+    turn_pair<kAll>(a.w, b.w, c[3], s[3]);
+}
+template <bool kAll>
+__device__ __forceinline__ void turn_bf16x2(uint32_t& a, uint32_t& b, const float* c,
+                                            const float* s) {
+    float a0 = __uint_as_float(a << 16), a1 = __uint_as_float(a & 0xffff0000u);
+    float b0 = __uint_as_float(b << 16), b1 = __uint_as_float(b & 0xffff0000u);
+    turn_pair<kAll>(a0, b0, c[0], s[0]);
+    turn_pair<kAll>(a1, b1, c[1], s[1]);
+    const __nv_bfloat162 ha = __floats2bfloat162_rn(a0, a1), hb = __floats2bfloat162_rn(b0, b1);
+    a = *reinterpret_cast<const uint32_t*>(&ha);
+    b = *reinterpret_cast<const uint32_t*>(&hb);
+}
+template <typename T, bool kAll>
+__device__ __forceinline__ void turn_row(uint4& a, uint4& b, const float* c, const float* s) {
+    turn_bf16x2<kAll>(a.x, b.x, c, s);
+    turn_bf16x2<kAll>(a.y, b.y, c + 2, s + 2);
+    turn_bf16x2<kAll>(a.z, b.z, c + 4, s + 4);
+    turn_bf16x2<kAll>(a.w, b.w, c + 6, s + 6);
+}
 
 struct RopeShape {
     int64_t n_sites, n_tokens, rep;
     int n_heads;
     int lanes_log2;   // pair slices of a row: d/2 / V
     int rlanes_log2;  // row lanes: rows that a site's threads turn at once
-    int rows_cta;     // rows per CTA (grid.y splits the rest)
+    int64_t rows_cta; // rows per CTA (grid.y splits the rest)
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_axes_kernel(
     const __grid_constant__ Params p, const __grid_constant__ AxisMap am, RopeShape sh,
     const int32_t* __restrict__ pos, const T* x, T* y) {
     constexpr int V = Vec<T>::N;
@@ -44,6 +82,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
     const int half = p.d / 2, tid = threadIdx.x;
     const int sites_log2 = 8 - sh.lanes_log2 - sh.rlanes_log2;
     const int64_t site0 = (int64_t)blockIdx.x << sites_log2;
+    const int u = (tid & ((1 << sh.lanes_log2) - 1)) * V;
+    const int rl = (tid >> sh.lanes_log2) & ((1 << sh.rlanes_log2) - 1);
+    const int sl = tid >> (sh.lanes_log2 + sh.rlanes_log2);
+    const int64_t site = site0 + sl;
+    const bool have = site < sh.n_sites;
+    const int64_t nb = site / sh.n_tokens, t = site % sh.n_tokens;
+    const int64_t rows = sh.rep * sh.n_heads;
+    const int step = 1 << sh.rlanes_log2;
+    const int64_t r0 = (int64_t)blockIdx.y * sh.rows_cta;
+    const int64_t r1 = r0 + sh.rows_cta < rows ? r0 + sh.rows_cta : rows;
+    typename Vec<T>::Raw ra[kBatch], rb[kBatch];
+    auto at = [&](int64_t rr) {
+        const int64_t r = sh.rep == 1 ? 0 : rr / sh.n_heads, h = rr - r * sh.n_heads;
+        return (((nb * sh.rep + r) * sh.n_tokens + t) * sh.n_heads + h) * p.d + u;
+    };
+    auto load = [&](int64_t rr) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t ri = rr + (int64_t)i * step;
+            if (have && ri < r1) {
+                const T* src = x + at(ri);
+                ra[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(src);
+                rb[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(src + half);
+            }
+        }
+    };
+    load(r0 + rl);  // on their way while the angles are made
     {
         // a thread makes one pair's angles only: the pair's axis and frequency are
         // read once (their index differs from lane to lane, which the constant
@@ -51,61 +116,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
         const int pair = tid & (half - 1), ax = am.axis[pair];
         const double freq = p.inv_freq[pair];
         for (int i = tid; i < half << sites_log2; i += kRopeThreads) {
-            const int64_t site = site0 + i / half;
-            float c = 1.f, sn = 0.f;
-            if (ax >= 0 && site < sh.n_sites) turn_cs((double)pos[ax * sh.n_sites + site], freq, c, sn);
+            const int64_t si = site0 + i / half;
+            float c = kNoTurn, sn = 0.f;
+            if (ax >= 0 && si < sh.n_sites) turn_cs((double)pos[ax * sh.n_sites + si], freq, c, sn);
             s_c[i] = c;
             s_s[i] = sn * am.sign;
         }
     }
     __syncthreads();
-    const int u = (tid & ((1 << sh.lanes_log2) - 1)) * V;
-    const int rl = (tid >> sh.lanes_log2) & ((1 << sh.rlanes_log2) - 1);
-    const int sl = tid >> (sh.lanes_log2 + sh.rlanes_log2);
-    const int64_t site = site0 + sl;
-    if (site >= sh.n_sites) return;
+    if (!have) return;
     float c[V], s[V];
-    unsigned turn = 0;  // bit e: pair u + e is rotated
+    bool all = true;  // of the thread's pairs are rotated
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        c[e] = s_c[sl * half + u + e];
-        s[e] = s_s[sl * half + u + e];
-        turn |= (am.axis[u + e] >= 0 ? 1u : 0u) << e;
+    for (int e = 0; e < V; e += 4) {
+        *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(s_c + sl * half + u + e);
+        *reinterpret_cast<float4*>(s + e) = *reinterpret_cast<const float4*>(s_s + sl * half + u + e);
     }
-    const int64_t nb = site / sh.n_tokens, t = site % sh.n_tokens;
-    const int64_t rows = sh.rep * sh.n_heads;
-    const int step = 1 << sh.rlanes_log2;
-    for (int64_t z = blockIdx.y; z * sh.rows_cta < rows; z += gridDim.y) {
-        const int64_t r1 = (z + 1) * sh.rows_cta < rows ? (z + 1) * sh.rows_cta : rows;
-        for (int64_t rr = z * sh.rows_cta + rl; rr < r1; rr += (int64_t)step * kBatch) {
-            int64_t o[kBatch];
-            typename Vec<T>::Raw ra[kBatch], rb[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int64_t ri = rr + (int64_t)i * step;
-                const int64_t r = sh.rep == 1 ? 0 : ri / sh.n_heads, h = ri - r * sh.n_heads;
-                o[i] = (((nb * sh.rep + r) * sh.n_tokens + t) * sh.n_heads + h) * p.d + u;
-                if (ri < r1) {
-                    ra[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(x + o[i]);
-                    rb[i] = *reinterpret_cast<const typename Vec<T>::Raw*>(x + o[i] + half);
-                }
-            }
+    for (int e = 0; e < V; ++e) all &= c[e] != kNoTurn;
+    for (int64_t rr = r0 + rl; rr < r1; rr += (int64_t)step * kBatch) {
+        if (rr != r0 + rl) load(rr);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (rr + (int64_t)i * step < r1) {
-                    float a[V], b[V], ya[V], yb[V];
-                    Vec<T>::unpack(ra[i], a);
-                    Vec<T>::unpack(rb[i], b);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        // an unrotated pair is copied, infinities among it
-                        const bool on = (turn >> e) & 1u;
-                        ya[e] = on ? a[e] * c[e] - b[e] * s[e] : a[e];
-                        yb[e] = on ? a[e] * s[e] + b[e] * c[e] : b[e];
-                    }
-                    Vec<T>::store(y + o[i], ya);
-                    Vec<T>::store(y + o[i] + half, yb);
-                }
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t ri = rr + (int64_t)i * step;
+            if (ri < r1) {
+                if (all)
+                    turn_row<T, true>(ra[i], rb[i], c, s);
+                else
+                    turn_row<T, false>(ra[i], rb[i], c, s);
+                T* dst = y + at(ri);
+                *reinterpret_cast<typename Vec<T>::Raw*>(dst) = ra[i];
+                *reinterpret_cast<typename Vec<T>::Raw*>(dst + half) = rb[i];
             }
         }
     }
@@ -329,6 +370,12 @@ cudaError_t launch_rope_axes(const Params& p, const AxisMap& am, const int32_t* 
     while (sh.lanes_log2 + sh.rlanes_log2 < 8 && (2 << sh.rlanes_log2) <= rows &&
            (sh.rlanes_log2 < 3 || (1 << (8 - sh.lanes_log2 - sh.rlanes_log2)) > sh.n_sites))
         ++sh.rlanes_log2;
+    // fewer where the last rows would leave more than an eighth of the lanes idle
+    while (sh.rlanes_log2 > 0) {
+        const int64_t rl = (int64_t)1 << sh.rlanes_log2, turns = (rows + rl - 1) / rl;
+        if (8 * (turns * rl - rows) <= turns * rl) break;
+        --sh.rlanes_log2;
+    }
     const int sites_log2 = 8 - sh.lanes_log2 - sh.rlanes_log2;
     const int64_t bx = (sh.n_sites + (1 << sites_log2) - 1) >> sites_log2;
     // Rows per CTA: one batch while the grid is short of two CTAs per SM (the
@@ -336,10 +383,10 @@ cudaError_t launch_rope_axes(const Params& p, const AxisMap& am, const int32_t* 
     // site's rows once it fills the GPU.
     int64_t per = (int64_t)1 << sh.rlanes_log2;
     while (per < rows && bx * ((rows + per - 1) / per) > 2 * 148) per *= 2;
-    sh.rows_cta = (int)(per < (1 << 20) ? per : (1 << 20));
-    const int64_t by = (rows + sh.rows_cta - 1) / sh.rows_cta;
+    while ((rows + per - 1) / per > 65535) per *= 2;
+    sh.rows_cta = per;
     if (bx > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)bx, (unsigned)(by < 65535 ? by : 65535));
+    const dim3 grid((unsigned)bx, (unsigned)((rows + per - 1) / per));
     using bf = __nv_bfloat16;
     if (p.dtype == HGA_BF16)
         rope_axes_kernel<bf><<<grid, kRopeThreads, 0, st>>>(p, am, sh, positions, (const bf*)x,
