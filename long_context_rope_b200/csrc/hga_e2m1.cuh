@@ -88,38 +88,64 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
+// The tensor scale with what a block's scale needs of it. slow: its quotients
+// by an ordinary divide (a magnitude whose reciprocal or remainders could leave
+// fp32's normal range).
+struct TensorScale {
+    float ts, six, inv_six;
+    bool slow;
+};
+
+__device__ __forceinline__ TensorScale tensor_scale(float ts) {
+    return {ts, 6.f * ts, __frcp_rn(6.f * ts), !(ts > 0x1p-80f && ts < 0x1p80f)};
+}
+
+// x / d, correctly rounded, with inv = 1 / d rounded: the product, then
+// Markstein's correction by the exact remainder (whose sign is taken so that a
+// zero keeps its own). Halfway quotients, exact ones among them, are met
+// exactly. For normal d and inv, and |x / d| well inside fp32's range.
+__device__ __forceinline__ float quotient(float x, float d, float inv) {
+    const float q = x * inv;
+    return fmaf(-fmaf(q, d, -x), inv, q);
+}
+
 // A block's scale by the rounding that hga_store_kv states: its code, S = its
-// value times the tensor scale, 1 / S. none: all codes 0 (a zero scale, or a
-// NaN or infinity in the block, whose scale is then NaN). slow: quotients by
-// an ordinary divide (saturated scales, whose quotients may be huge, and
-// magnitudes whose reciprocal or remainder could leave fp32's normal range).
+// value times the tensor scale, 1 / S. none: all codes are 0 (a zero scale, or a
+// NaN or an infinity in the block, whose scale is then NaN). slow: as above, or
+// a saturated scale, whose quotients may be huge.
 struct Scale {
     uint32_t code;
     float S, inv;
     bool none, slow;
 };
 
-__device__ __forceinline__ Scale block_scale(float amax, float ts) {
+__device__ __forceinline__ Scale block_scale(float amax, const TensorScale& t) {
     Scale r;
     const bool finite = amax < INFINITY;
-    r.code = finite ? scale_code(amax / (6.f * ts)) : 0x7fu;
-    r.S = scale_value(r.code) * ts;
+    // at most 512 before the correction, so that it cannot overflow; anything
+    // above 448 is 448
+    const float q = fminf(amax * t.inv_six, 512.f);
+    const float a = t.slow ? amax / t.six : fmaf(-fmaf(q, t.six, -amax), t.inv_six, q);
+    r.code = finite ? scale_code(a) : 0x7fu;
+    r.S = scale_value(r.code) * t.ts;
     r.none = !(r.S > 0.f);  // NaN too
     if (r.none && finite) r.code = 0u;
-    r.slow = r.code == 0x7eu || r.S < 0x1p-80f || r.S > 0x1p80f;
+    r.slow = t.slow || r.code == 0x7eu;
     r.inv = __frcp_rn(r.S);
     return r;
 }
 
-// x / S, correctly rounded: the product with the rounded reciprocal, then
-// Markstein's correction by the exact remainder. Of bf16 elements and a
-// power-of-two tensor scale the quotients that lie halfway between two codes
-// are met exactly. (A divide per element made the store compute-bound.)
-__device__ __forceinline__ float quotient(float x, const Scale& s) {
-    if (s.none) return 0.f;
-    if (s.slow) return x / s.S;
-    const float q = x * s.inv;
-    return copysignf(fmaf(fmaf(-q, s.S, x), s.inv, q), x);
+// Eight elements' codes under a scale.
+__device__ __forceinline__ uint32_t codes_of(const float* x, const Scale& s) {
+    float q[8];
+    if (s.slow) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = x[e] / s.S;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = quotient(x[e], s.S, s.inv);
+    }
+    return s.none ? 0u : f32x8_to_codes(q);
 }
 
 }  // namespace e2m1

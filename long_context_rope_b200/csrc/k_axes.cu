@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
     __shared__ int s_pos[HGA_MAX_AXES][8 * kGroupRows];   // groups_per_chunk <= 8
     __shared__ int64_t s_psum[HGA_MAX_AXES][8];
     __shared__ alignas(16) float s_mc[9][half], s_ms[9][half];  // mean angles: groups, chunk
-    __shared__ alignas(16) float s_sum[8][D];
+    __shared__ alignas(16) float s_sum[2][8][D];           // per head parity: the groups' sums
     const int G = p.G, tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
     const int u = lane & (L - 1), q = lane / L;
     const int ch = chunk_begin + blockIdx.x;
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
                 const double freq = p.inv_freq[pair];
                 const bool low = pair >= p.F;
                 if (ax >= 0 && (!low || k_rot != nullptr))
+#pragma unroll 2
                     for (int r = tid / half; r < n_rows; r += per)
                         turn_cs((double)s_pos[ax][r], freq, tc[table_at(r, pair, half)],
                                 ts[table_at(r, pair, half)]);
@@ -264,6 +265,8 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
         each |= (on && !low ? 1u : 0u) << e;
         mean |= (on && low ? 1u : 0u) << e;
     }
+    // the whole warp's pairs are rotated token by token (the rotated keys are wanted)
+    const bool all = __all_sync(0xffffffffu, turn == (1u << V) - 1u) != 0;
     __syncthreads();
 
     for (int h = h0; h < h1; ++h) {
@@ -286,9 +289,13 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
                 }
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const bool on = (turn >> e) & 1u, in = (each >> e) & 1u;
-                    const float ra = on ? a[e] * c[e] - bb[e] * sn[e] : a[e];
-                    const float rb = on ? a[e] * sn[e] + bb[e] * c[e] : bb[e];
+                    const bool in = (each >> e) & 1u;
+                    float ra = a[e] * c[e] - bb[e] * sn[e], rb = a[e] * sn[e] + bb[e] * c[e];
+                    if (!all) {
+                        const bool on = (turn >> e) & 1u;
+                        ra = on ? ra : a[e];
+                        rb = on ? rb : bb[e];
+                    }
                     acc0[e] += in ? ra : a[e];
                     acc1[e] += in ? rb : bb[e];
                     a[e] = ra;
@@ -328,9 +335,9 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
             finish(acc0, acc1, g, n_g, gs + ((bh * p.nC + ch) * G + g) * (int64_t)D);
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
-                *reinterpret_cast<float4*>(&s_sum[g][u * V + e]) =
+                *reinterpret_cast<float4*>(&s_sum[h & 1][g][u * V + e]) =
                     *reinterpret_cast<const float4*>(acc0 + e);
-                *reinterpret_cast<float4*>(&s_sum[g][half + u * V + e]) =
+                *reinterpret_cast<float4*>(&s_sum[h & 1][g][half + u * V + e]) =
                     *reinterpret_cast<const float4*>(acc1 + e);
             }
         }
@@ -340,13 +347,13 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
             for (int e = 0; e < V; ++e) {
                 acc0[e] = acc1[e] = 0.f;
                 for (int y = 0; y < G; ++y) {
-                    acc0[e] += s_sum[y][u * V + e];
-                    acc1[e] += s_sum[y][half + u * V + e];
+                    acc0[e] += s_sum[h & 1][y][u * V + e];
+                    acc1[e] += s_sum[h & 1][y][half + u * V + e];
                 }
             }
             finish(acc0, acc1, 8, n_rows, cs + (bh * p.nC + ch) * (int64_t)D);
         }
-        __syncthreads();
+        // the other parity's sums are free: their readers came through this barrier
     }
 }
 

@@ -23,25 +23,48 @@ using bf = __nv_bfloat16;
 
 constexpr int kStoreThreads = 256;
 
-// Where token `at` of unit bh starts in a store: its page; *row: within it.
-__device__ __forceinline__ int64_t page_of(const Params& p, int64_t bh, int64_t at, int* row) {
-    *row = (int)(at % kGroupRows);
-    return bh * p.kv_slab + (at / kGroupRows) * kE2m1Page;
+// Division of row numbers by the tokens per unit. 32 bits (numbers below 2^31):
+// by multiplication, n / d = (mulhi(n, m) + n) >> s with s = ceil(log2 d) and m =
+// floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery).
+struct Div32 {
+    using I = uint32_t;
+    uint32_t d, m, s;
+    explicit Div32(int64_t tokens) : d((uint32_t)tokens), s(0) {
+        while (((uint64_t)1 << s) < d) ++s;
+        m = (uint32_t)(((uint64_t)1 << 32) * (((uint64_t)1 << s) - d) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        return (__umulhi(n, m) + n) >> s;
+    }
+};
+struct Div64 {
+    using I = uint64_t;
+    uint64_t d;
+    explicit Div64(int64_t tokens) : d((uint64_t)tokens) {}
+    __device__ __forceinline__ uint64_t operator()(uint64_t n) const { return n / d; }
+};
+
+// Where a row of a call's token t of unit bh starts in a store: its page; *row:
+// within it.
+__device__ __forceinline__ int64_t page_of(const Params& p, int64_t bh, int at, int* row) {
+    *row = at % kGroupRows;
+    return bh * p.kv_slab + (int64_t)(at / kGroupRows) * kE2m1Page;
 }
 
 // Rows as they are. Item = (row, block): row * 8 + block, so eight lanes hold
 // the eight blocks of a row; its scales are written four bytes at a time. I: an
 // unsigned type that holds the item count and a grid more.
-template <typename I>
+template <typename Div, typename I = typename Div::I>
 __device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8_t* store, float ts,
-                                           int64_t pos0, I n_tokens, I n_rows) {
+                                           int pos0, const Div& unit, I n_rows) {
+    const e2m1::TensorScale tensor = e2m1::tensor_scale(ts);
     const int blk = threadIdx.x & 7;
     const I n_items = n_rows * 8;
     // whole warps stay to the end: their lanes exchange scales
     for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; (it & ~(I)31) < n_items;
          it += (I)gridDim.x * kStoreThreads) {
         const bool ok = it < n_items;
-        const I row = ok ? it >> 3 : 0, bh = row / n_tokens, t = row - bh * n_tokens;
+        const I row = ok ? it >> 3 : 0, bh = unit(row), t = row - bh * unit.d;
         const uint4* src16 = reinterpret_cast<const uint4*>(src + (int64_t)row * 128 + kBlock * blk);
         const uint4 r0 = src16[0], r1 = src16[1];
         const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
@@ -50,17 +73,15 @@ __device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
         m = max(m >> 16, m & 0xffffu);
-        const e2m1::Scale sc = e2m1::block_scale(__uint_as_float(m << 16), ts);
+        const e2m1::Scale sc = e2m1::block_scale(__uint_as_float(m << 16), tensor);
         float x[kBlock];
         bf16x8_to_f32(r0, x);
         bf16x8_to_f32(r1, x + 8);
-#pragma unroll
-        for (int e = 0; e < kBlock; ++e) x[e] = e2m1::quotient(x[e], sc);
         int pr;
-        uint8_t* pg = store + page_of(p, bh, pos0 + t, &pr);
+        uint8_t* pg = store + page_of(p, bh, pos0 + (int)t, &pr);
         if (ok)
             *reinterpret_cast<uint2*>(pg + e2m1::code_at(pr, kBlock * blk)) =
-                make_uint2(e2m1::f32x8_to_codes(x), e2m1::f32x8_to_codes(x + 8));
+                make_uint2(e2m1::codes_of(x, sc), e2m1::codes_of(x + 8, sc));
         uint32_t four = sc.code << (8 * (blk & 3));
         four |= __shfl_xor_sync(0xffffffffu, four, 1);
         four |= __shfl_xor_sync(0xffffffffu, four, 2);
@@ -70,10 +91,11 @@ __device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8
 
 // Keys rotated on the way. 16 lanes a row, each with 4 rotary pairs: dims
 // 4l .. + 3 and 64 + 4l .. + 3. Item = (row, lane): row * 16 + lane.
-template <typename I>
+template <typename Div, typename I = typename Div::I>
 __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am,
                                               const int32_t* pos, const bf* k, uint8_t* ks,
-                                              int64_t pos0, I n_tokens, I n_rows) {
+                                              int pos0, const Div& unit, I n_rows) {
+    const e2m1::TensorScale tensor = e2m1::tensor_scale(p.k_scale);
     const int l = threadIdx.x & 15;
     const I n_items = n_rows * 16;
     // this lane's pairs, read once (the constant cache serves one index at a time)
@@ -87,8 +109,8 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
     for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; (it & ~(I)31) < n_items;
          it += (I)gridDim.x * kStoreThreads) {
         const bool ok = it < n_items;
-        const I row = ok ? it >> 4 : 0, bh = row / n_tokens, t = row - bh * n_tokens;
-        const int64_t at = pos0 + t;
+        const I row = ok ? it >> 4 : 0, bh = unit(row), t = row - bh * unit.d;
+        const int at = pos0 + (int)t;
         const uint2* src8 = reinterpret_cast<const uint2*>(k + (int64_t)row * 128 + 4 * l);
         const uint2 lo = src8[0], hi = src8[16];
         const uint32_t wl[2] = {lo.x, lo.y}, wh[2] = {hi.x, hi.y};
@@ -101,7 +123,7 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
             x[1][e] = b;
             if (axis[e] >= 0) {
                 const double at_axis =
-                    pos ? (double)pos[((int64_t)axis[e] * p.B + bh / p.Hkv) * n_tokens + t] : (double)at;
+                    pos ? (double)pos[((int64_t)axis[e] * p.B + bh / p.Hkv) * unit.d + t] : (double)at;
                 double c, sn;
                 turn_cs64(at_axis, freq[e], c, sn);
                 x[0][e] = (float)((double)a * c - (double)b * sn);
@@ -117,11 +139,9 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
             for (int e = 0; e < 4; ++e) amax = e2m1::max_nan(amax, fabsf(x[y][e]));
             amax = e2m1::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = e2m1::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const e2m1::Scale sc = e2m1::block_scale(amax, p.k_scale);
-            float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = e2m1::quotient(x[y][e], sc);
-            const uint32_t w = e2m1::f32x8_to_codes(q) & 0xffffu;
+            const e2m1::Scale sc = e2m1::block_scale(amax, tensor);
+            const float four[8] = {x[y][0], x[y][1], x[y][2], x[y][3], 0.f, 0.f, 0.f, 0.f};
+            const uint32_t w = e2m1::codes_of(four, sc) & 0xffffu;
             // four lanes' 16 bits of codes to the first of them
             const uint32_t w1 = w | (__shfl_down_sync(0xffffffffu, w, 1) << 16);
             const uint32_t w2 = __shfl_down_sync(0xffffffffu, w1, 2);
@@ -135,28 +155,29 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
 }
 
 // grid.y = 0: keys, 1: values.
-template <typename I, bool kRotate>
+template <typename Div, bool kRotate>
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(
     const __grid_constant__ Params p, const __grid_constant__ AxisMap am,
     const int32_t* __restrict__ pos, const bf* __restrict__ k, const bf* __restrict__ v,
-    uint8_t* __restrict__ ks, uint8_t* __restrict__ vs, int64_t pos0, I n_tokens, I n_rows) {
+    uint8_t* __restrict__ ks, uint8_t* __restrict__ vs, int pos0, Div unit,
+    typename Div::I n_rows) {
     if (blockIdx.y == 1)
-        store_rows<I>(p, v, vs, p.v_scale, pos0, n_tokens, n_rows);
+        store_rows(p, v, vs, p.v_scale, pos0, unit, n_rows);
     else if (kRotate)
-        store_rotated<I>(p, am, pos, k, ks, pos0, n_tokens, n_rows);
+        store_rotated(p, am, pos, k, ks, pos0, unit, n_rows);
     else
-        store_rows<I>(p, k, ks, p.k_scale, pos0, n_tokens, n_rows);
+        store_rows(p, k, ks, p.k_scale, pos0, unit, n_rows);
 }
 
 // grid.y = 0: keys, 1: values. Item = (row, 8 dims): row * 16 + piece; a
 // thread has kLoadItems of them in flight, a grid apart.
 constexpr int kLoadItems = 4;
 
-template <typename I>
+template <typename Div, typename I = typename Div::I>
 __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
     const __grid_constant__ Params p, const uint8_t* __restrict__ ks,
-    const uint8_t* __restrict__ vs, bf* __restrict__ k, bf* __restrict__ v, int64_t pos0,
-    I n_tokens, I n_items) {
+    const uint8_t* __restrict__ vs, bf* __restrict__ k, bf* __restrict__ v, int pos0,
+    Div unit, I n_items) {
     const uint8_t* store = blockIdx.y ? vs : ks;
     bf* dst = blockIdx.y ? v : k;
     const float ts = blockIdx.y ? p.v_scale : p.k_scale;
@@ -169,9 +190,9 @@ __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
         for (int i = 0; i < kLoadItems; ++i) {
             const I x = it + step * i;
             if (x < n_items) {
-                const I row = x >> 4, bh = row / n_tokens, t = row - bh * n_tokens;
+                const I row = x >> 4, bh = unit(row), t = row - bh * unit.d;
                 int pr;
-                const uint8_t* pg = store + page_of(p, bh, pos0 + t, &pr);
+                const uint8_t* pg = store + page_of(p, bh, pos0 + (int)t, &pr);
                 w[i] = *reinterpret_cast<const uint32_t*>(pg + e2m1::code_at(pr, 8 * pc));
                 sc[i] = pg[e2m1::scale_at(pr, pc >> 1)];
             }
@@ -203,14 +224,14 @@ unsigned grid_of(int64_t items) {
     return (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16);
 }
 
-// f(an unsigned item type): 32 bits where items and the grids' strides past
-// them fit.
+// f(the division for a call's row numbers): 32 bits where items and the grids'
+// strides past them fit.
 template <typename F>
-void with_index(int64_t items, F f) {
+void with_division(int64_t items, int64_t n_tokens, F f) {
     if (items < (int64_t)1 << 30)
-        f(uint32_t());
+        f(Div32(n_tokens));
     else
-        f(uint64_t());
+        f(Div64(n_tokens));
 }
 
 }  // namespace
@@ -220,17 +241,17 @@ cudaError_t launch_store_kv(const Params& p, const AxisMap& am, const int32_t* p
                             int64_t pos0, int64_t n_tokens, cudaStream_t st) {
     const int64_t rows = (int64_t)p.B * p.Hkv * n_tokens;
     const bool rotate = am.n_axes > 0;
-    with_index(rows * 16, [&](auto i) {
-        using I = decltype(i);
+    with_division(rows * 16, n_tokens, [&](auto unit) {
+        using Div = decltype(unit);
         auto run = [&](auto* kernel, int lanes) {
             kernel<<<dim3(grid_of(rows * lanes), 2), kStoreThreads, 0, st>>>(
                 p, am, positions, (const bf*)k, (const bf*)v, (uint8_t*)k_store, (uint8_t*)v_store,
-                pos0, (I)n_tokens, (I)rows);
+                (int)pos0, unit, (typename Div::I)rows);
         };
         if (rotate)
-            run(store_kv_kernel<I, true>, 16);
+            run(store_kv_kernel<Div, true>, 16);
         else
-            run(store_kv_kernel<I, false>, 8);
+            run(store_kv_kernel<Div, false>, 8);
     });
     return cudaGetLastError();
 }
@@ -238,12 +259,12 @@ cudaError_t launch_store_kv(const Params& p, const AxisMap& am, const int32_t* p
 cudaError_t launch_load_kv(const Params& p, const void* k_store, const void* v_store, void* k,
                            void* v, int64_t pos0, int64_t n_tokens, cudaStream_t st) {
     const int64_t rows = (int64_t)p.B * p.Hkv * n_tokens;
-    with_index(rows * 16, [&](auto i) {
-        using I = decltype(i);
+    with_division(rows * 16, n_tokens, [&](auto unit) {
+        using Div = decltype(unit);
         const dim3 grid(grid_of((rows * 16 + kLoadItems - 1) / kLoadItems), 2);
-        load_kv_kernel<I><<<grid, kStoreThreads, 0, st>>>(
-            p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, pos0, (I)n_tokens,
-            (I)(rows * 16));
+        load_kv_kernel<Div><<<grid, kStoreThreads, 0, st>>>(
+            p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, (int)pos0, unit,
+            (typename Div::I)(rows * 16));
     });
     return cudaGetLastError();
 }
