@@ -64,12 +64,20 @@ __host__ __device__ constexpr int64_t page_slab(int64_t rows) {
     return (rows + kGroupRows - 1) / kGroupRows * kE2m1Page;
 }
 
-// A page pair of one block and the position of its first token.
+// A lane's view of a block's page pair: K page + 16 lane and V page + 16 (lane -
+// 8) (a base that is offset once costs one multiply-add per page and tensor).
 struct PageRef {
     const uint8_t* k;
     const uint8_t* v;
-    int pos;
 };
+__device__ __forceinline__ PageRef lane_pages(const uint8_t* k, const uint8_t* v) {
+    const int lane = threadIdx.x & 31;
+    return {k + 16 * lane, v + 16 * (lane - 8)};
+}
+__device__ __forceinline__ PageRef page_at(const PageRef& base, int page) {
+    const int64_t at = (int64_t)page * kE2m1Page;
+    return {base.k + at, base.v + at};
+}
 
 __device__ __forceinline__ int swz(int tile) { return 2 * tile + (tile & 1); }
 
@@ -125,50 +133,68 @@ __device__ __forceinline__ void load_q_pages(const Params& p, const __nv_bfloat1
     }
 }
 
-// The warp's asynchronous copies of a page pair into a stage: piece i < 72 of
-// K, then of V.
-__device__ __forceinline__ void copy_pages(uint32_t stage, const PageRef& ref) {
+// The warp's asynchronous copies of a page pair into a stage: 72 pieces of K,
+// then 72 of V, piece lane + 32 u to dst[u].
+struct CopyPlan {
+    uint32_t dst[kPageCopies];
+};
+__device__ __forceinline__ CopyPlan copy_plan() {
     const int lane = threadIdx.x & 31;
+    CopyPlan c;
 #pragma unroll
     for (int u = 0; u < kPageCopies; ++u) {
-        const int i = lane + 32 * u;
-        const bool is_v = i >= kPageVecs;
-        const int pc = is_v ? i - kPageVecs : i;
-        const int off = pc < 64 ? code_piece(pc >> 4, pc & 15) : pc * 16;
-        if (i < 2 * kPageVecs)
-            ptx::cp_async16(stage + (is_v ? kE2m1Page : 0) + off, (is_v ? ref.v : ref.k) + pc * 16);
+        const int i = lane + 32 * u, pc = i >= kPageVecs ? i - kPageVecs : i;
+        c.dst[u] = (i >= kPageVecs ? kE2m1Page : 0) + (pc < 64 ? code_piece(pc >> 4, pc & 15) : pc * 16);
     }
+    return c;
+}
+__device__ __forceinline__ void copy_pages(const CopyPlan& c, uint32_t stage, const PageRef& r) {
+    static_assert(kPageVecs == 72 && kPageCopies == 5, "the split of the pieces over copies");
+    const int lane = threadIdx.x & 31;
+    ptx::cp_async16(stage + c.dst[0], r.k);
+    ptx::cp_async16(stage + c.dst[1], r.k + 512);
+    ptx::cp_async16(stage + c.dst[2], lane < 8 ? r.k + 1024 : r.v);
+    ptx::cp_async16(stage + c.dst[3], r.v + 512);
+    if (lane < 16) ptx::cp_async16(stage + c.dst[4], r.v + 1024);
 }
 
-// The warp's blocks 0 .. n - 1, block_of(i) their pages; qpos: the query's
-// position. Keys after it are masked, and their values' scales read as zero
-// (their rows may hold anything).
-template <typename BlockOf>
+// The warp's blocks 0 .. n - 1: page_of(i) their pages, pos_of(i) the position
+// of their first token; qpos: the query's position. Keys after it are masked,
+// and their values' scales read as zero (their rows may hold anything).
+template <typename PageOf, typename PosOf>
 __device__ __forceinline__ void consume_pages(const uint32_t (&qf)[8][2], const float (&sc)[2],
                                               uint8_t (*ring)[kPagePair], int n, int qpos,
-                                              BlockOf block_of, WarpAcc& acc) {
+                                              PageOf page_of, PosOf pos_of, WarpAcc& acc) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const CopyPlan plan = copy_plan();
+    const uint32_t ring0 = ptx::smem_u32(ring[0]);
     float mz[2] = {0.f, 0.f};  // the maximum, 0 while there is none
+    float top[2] = {-INFINITY, -INFINITY};  // the score above which it is raised
 #pragma unroll
     for (int d = 0; d < kPageStages; ++d) {
-        if (d < n) copy_pages(ptx::smem_u32(ring[d]), block_of(d));
+        if (d < n) copy_pages(plan, ring0 + d * kPagePair, page_of(d));
         ptx::cp_async_commit();
     }
-    int st = 0;
+    // this lane's places in a stage: its key rows g (and g + 8, 128 bytes on) and
+    // their scales; its value rows 2 t4 and 2 t4 + 1 (and 8 more) and theirs
+    const int key_at = code_piece(t4, g), key_sc = e2m1::scale_at(g, 2 * t4);
+    const int val_at[2] = {kE2m1Page + code_piece(g >> 1, 2 * t4) + 8 * (g & 1),
+                           kE2m1Page + code_piece(g >> 1, 2 * t4 + 1) + 8 * (g & 1)};
+    const int val_sc = kE2m1Page + e2m1::scale_at(2 * t4, g);
+    int st = 0;  // the stage's offset in the ring
     for (int i = 0; i < n; ++i) {
         ptx::cp_async_wait<kPageStages - 1>();
         __syncwarp();
-        const uint8_t* kb = ring[st];
-        const uint8_t* vb = kb + kE2m1Page;
-        const int kp = block_of(i).pos;
+        const uint8_t* stage = ring[0] + st;
+        const int kp = pos_of(i);
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
         {
-            const uint4 w0 = *reinterpret_cast<const uint4*>(kb + code_piece(t4, g));
-            const uint4 w1 = *reinterpret_cast<const uint4*>(kb + code_piece(t4, g + 8));
-            const uint32_t c0 = e2m1::scales_to_f16x2(
-                *reinterpret_cast<const uint16_t*>(kb + e2m1::scale_at(g, 2 * t4)));
-            const uint32_t c1 = e2m1::scales_to_f16x2(
-                *reinterpret_cast<const uint16_t*>(kb + e2m1::scale_at(g + 8, 2 * t4)));
+            const uint4 w0 = *reinterpret_cast<const uint4*>(stage + key_at);
+            const uint4 w1 = *reinterpret_cast<const uint4*>(stage + key_at + 128);
+            const uint32_t c0 =
+                e2m1::scales_to_f16x2(*reinterpret_cast<const uint16_t*>(stage + key_sc));
+            const uint32_t c1 =
+                e2m1::scales_to_f16x2(*reinterpret_cast<const uint16_t*>(stage + key_sc + 64));
             const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -195,8 +221,7 @@ __device__ __forceinline__ void consume_pages(const uint32_t (&qf)[8][2], const 
             if (kp + g > qpos) s[0] = s[1] = -INFINITY;
             if (kp + g + 8 > qpos) s[2] = s[3] = -INFINITY;
         }
-        const bool raise = s[0] > acc.m[0] + kRaise || s[2] > acc.m[0] + kRaise ||
-                           s[1] > acc.m[1] + kRaise || s[3] > acc.m[1] + kRaise;
+        const bool raise = fmaxf(s[0], s[2]) > top[0] || fmaxf(s[1], s[3]) > top[1];
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
@@ -208,6 +233,7 @@ __device__ __forceinline__ void consume_pages(const uint32_t (&qf)[8][2], const 
                 if (mn != -INFINITY) {
                     const float alpha = ptx::ex2_approx(acc.m[hh] - mn);  // 0 from -inf
                     acc.m[hh] = mz[hh] = mn;
+                    top[hh] = mn + kRaise;
                     acc.l[hh] *= alpha;
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
@@ -229,15 +255,17 @@ __device__ __forceinline__ void consume_pages(const uint32_t (&qf)[8][2], const 
             pb[k8] = ptx::movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h2));
         }
         {
-            const int r0 = 2 * t4;
-            uint2 w[4];         // keys r0, r0 + 1, r0 + 8, r0 + 9: dims 16 g .. + 15
+            uint2 w[4];         // keys 2 t4 + {0, 1, 8, 9}: dims 16 g .. + 15
             uint32_t c[4];      // their scale bytes
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int r = r0 + (x & 1) + 8 * (x >> 1);
-                w[x] = *reinterpret_cast<const uint2*>(vb + code_piece(g >> 1, r) + 8 * (g & 1));
-                c[x] = vb[e2m1::scale_at(r, g)];
-                if (partial && kp + r > qpos) c[x] = 0u;
+                w[x] = *reinterpret_cast<const uint2*>(stage + val_at[x & 1] + 128 * (x >> 1));
+                c[x] = stage[val_sc + 8 * (x & 1) + 64 * (x >> 1)];
+            }
+            if (partial) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (kp + 2 * t4 + (x & 1) + 8 * (x >> 1) > qpos) c[x] = 0u;
             }
             const uint32_t c0 = e2m1::scales_to_f16x2((uint16_t)(c[0] | (c[1] << 8)));
             const uint32_t c1 = e2m1::scales_to_f16x2((uint16_t)(c[2] | (c[3] << 8)));
@@ -265,9 +293,9 @@ __device__ __forceinline__ void consume_pages(const uint32_t (&qf)[8][2], const 
             }
         }
         __syncwarp();  // every lane is done with the stage
-        if (i + kPageStages < n) copy_pages(ptx::smem_u32(ring[st]), block_of(i + kPageStages));
+        if (i + kPageStages < n) copy_pages(plan, ring0 + st, page_of(i + kPageStages));
         ptx::cp_async_commit();
-        st = st + 1 == kPageStages ? 0 : st + 1;
+        st = st == (kPageStages - 1) * kPagePair ? 0 : st + kPagePair;
     }
 }
 

@@ -114,16 +114,15 @@ __global__ void __launch_bounds__(kPageThreads, 2) attend_pages_kernel(
 
     dec::WarpAcc acc;
     dec::acc_init(acc);
+    const dec::PageRef rbase = dec::lane_pages(res.k + kvh * res.slab, res.v + kvh * res.slab);
+    const dec::PageRef gbase = dec::lane_pages(gat.k + bh * gat.slab, gat.v + bh * gat.slab);
     dec::consume_pages(
         qf, sc, sm.u.page[warp], n, p.q_begin,
         [&](int i) {
-            const int2 e = sm.blk[warp][i];
-            const bool g = (e.x & kSrcGathered) != 0;
-            const int64_t at = (g ? bh * gat.slab : kvh * res.slab) +
-                               (int64_t)(e.x & ~kSrcGathered) * kE2m1Page;
-            return dec::PageRef{(g ? gat.k : res.k) + at, (g ? gat.v : res.v) + at, e.y};
+            const int page = sm.blk[warp][i].x;
+            return dec::page_at((page & kSrcGathered) ? gbase : rbase, page & ~kSrcGathered);
         },
-        acc);
+        [&](int i) { return sm.blk[warp][i].y; }, acc);
     dec::merge_pages(sm, cluster, p, acc, b, h, out);
 }
 

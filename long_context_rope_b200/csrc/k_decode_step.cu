@@ -469,18 +469,18 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
             uint32_t qf[8][2];
             float sc[2];
             dec::load_q_pages(p, q, b, h, qf, sc);
+            const dec::PageRef dbase =
+                dec::lane_pages(src.k + kvh * src.slab, src.v + kvh * src.slab);
+            const dec::PageRef hbase = dec::lane_pages((const uint8_t*)k_host + kvh * p.kv_slab,
+                                                       (const uint8_t*)v_host + kvh * p.kv_slab);
             dec::consume_pages(
                 qf, sc, sm.u.page[warp], (nloc - warp + kConsumers - 1) / kConsumers, p.q_begin,
                 [&](int i) {
                     const int x = warp + kConsumers * i;
-                    const bool host = host_tier && x >= nf_loc;
-                    const int64_t at = kvh * (host ? p.kv_slab : src.slab) +
-                                       (int64_t)(sm.blk_row[x] / kGroupRows) * kE2m1Page;
-                    return dec::PageRef{(host ? (const uint8_t*)k_host : src.k) + at,
-                                        (host ? (const uint8_t*)v_host : src.v) + at,
-                                        sm.blk_pos[x]};
+                    return dec::page_at(host_tier && x >= nf_loc ? hbase : dbase,
+                                        sm.blk_row[x] / kGroupRows);
                 },
-                acc);
+                [&](int i) { return sm.blk_pos[warp + kConsumers * i]; }, acc);
         }
         dec::merge_pages(sm, cluster, p, acc, b, h, out);
     } else {
