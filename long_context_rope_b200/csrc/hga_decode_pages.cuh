@@ -44,12 +44,14 @@ constexpr int kPageVecs = kE2m1Page / 16;     // 72 16-byte pieces
 constexpr int kPageCopies = (2 * kPageVecs + 31) / 32;
 constexpr float kRaise = 8.0f;
 
+// kWarps: warps of the CTA that take pages.
+template <int kWarps>
 struct PageSmem {
     union {
-        alignas(128) uint8_t page[kConsumers][kPageStages][kPagePair];
-        alignas(16) float part[kConsumers][8][kOStride];  // per warp and head: O, reused
+        alignas(128) uint8_t page[kWarps][kPageStages][kPagePair];
+        alignas(16) float part[kWarps][8][kOStride];  // per warp and head: O, reused
     } u;
-    float m[kConsumers][8], l[kConsumers][8];  // per warp and head: max, sum
+    float m[kWarps][8], l[kWarps][8];          // per warp and head: max, sum
     alignas(16) Owned owned;                   // partials of the heads this CTA finalises
 };
 
@@ -311,10 +313,11 @@ __device__ __forceinline__ void store_places(const Params& p, float4 num, float 
     for (int i = 0; i < 4; ++i) row[d0 + 16 * i] = __float2bfloat16_rn(v[i] * inv);
 }
 
-// All threads of the CTA: joins the partials of the CTA's eight warps, then of
+// All threads of the CTA: joins the partials of the CTA's warps, then of
 // the cluster's CTAs (CTA n % CL finalises head n), and writes the output
 // rows. Sums in warp and CTA order.
-__device__ __forceinline__ void merge_pages(PageSmem& sm, cg::cluster_group& cluster,
+template <int kWarps>
+__device__ __forceinline__ void merge_pages(PageSmem<kWarps>& sm, cg::cluster_group& cluster,
                                             const Params& p, const WarpAcc& acc, int b, int h,
                                             __nv_bfloat16* out) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
@@ -322,7 +325,7 @@ __device__ __forceinline__ void merge_pages(PageSmem& sm, cg::cluster_group& clu
     const int per = owned_per_cta(CL);
     __nv_bfloat16* orow = out + ((int64_t)b * p.q_len * p.Hq + (int64_t)h * p.gq) * kD;
     __syncthreads();  // every warp is done with its pages
-    if (warp < kConsumers) {
+    if (warp < kWarps) {
         float* o = sm.u.part[warp][2 * t4];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -342,7 +345,6 @@ __device__ __forceinline__ void merge_pages(PageSmem& sm, cg::cluster_group& clu
         }
     }
     __syncthreads();
-    // warp n: head n
     auto join = [&](int count, auto m_of, auto l_of, auto o_of, float& M, float4& num, float& den) {
         M = -INFINITY;
         for (int w = 0; w < count; ++w) M = fmaxf(M, m_of(w));
@@ -361,16 +363,17 @@ __device__ __forceinline__ void merge_pages(PageSmem& sm, cg::cluster_group& clu
     };
     float M, den;
     float4 num;
-    if (warp < p.gq) {
+    // warp w: heads w, w + kWarps, ..
+    for (int n = warp; warp < kWarps && n < p.gq; n += kWarps) {
         join(
-            kConsumers, [&](int w) { return sm.m[w][warp]; }, [&](int w) { return sm.l[w][warp]; },
-            [&](int w) { return *reinterpret_cast<const float4*>(&sm.u.part[w][warp][4 * lane]); },
-            M, num, den);
+            kWarps, [&](int w) { return sm.m[w][n]; }, [&](int w) { return sm.l[w][n]; },
+            [&](int w) { return *reinterpret_cast<const float4*>(&sm.u.part[w][n][4 * lane]); }, M,
+            num, den);
         if (CL == 1) {
-            store_places(p, num, den, orow + warp * kD);
+            store_places(p, num, den, orow + n * kD);
         } else {
-            Owned* dst = cluster.map_shared_rank(&sm.owned, warp % CL);
-            const int slot = r * per + warp / CL;
+            Owned* dst = cluster.map_shared_rank(&sm.owned, n % CL);
+            const int slot = r * per + n / CL;
             *reinterpret_cast<float4*>(&dst->o[slot][4 * lane]) = num;
             if (lane == 0) {
                 dst->m[slot] = M;
@@ -380,16 +383,15 @@ __device__ __forceinline__ void merge_pages(PageSmem& sm, cg::cluster_group& clu
     }
     if (CL == 1) return;
     cluster.sync();  // every partial is in its owner's shared memory
-    const int n = r + warp * CL;
-    if (warp < kConsumers && n < p.gq) {
+    for (int k = warp; warp < kWarps && r + k * CL < p.gq; k += kWarps) {
         join(
-            CL, [&](int c) { return sm.owned.m[c * per + warp]; },
-            [&](int c) { return sm.owned.l[c * per + warp]; },
+            CL, [&](int c) { return sm.owned.m[c * per + k]; },
+            [&](int c) { return sm.owned.l[c * per + k]; },
             [&](int c) {
-                return *reinterpret_cast<const float4*>(&sm.owned.o[c * per + warp][4 * lane]);
+                return *reinterpret_cast<const float4*>(&sm.owned.o[c * per + k][4 * lane]);
             },
             M, num, den);
-        store_places(p, num, den, orow + n * kD);
+        store_places(p, num, den, orow + (r + k * CL) * kD);
     }
 }
 

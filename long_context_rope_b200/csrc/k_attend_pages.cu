@@ -6,11 +6,15 @@
 // exact token set. Every page of the set is read once (2304 bytes for 16 keys
 // and values), and the query heads of a KV head share each load (GQA).
 //
-// One cluster of CL CTAs of eight warps per (sequence, KV head): CL as large
-// as keeps every unit's cluster resident at once (two CTAs per SM), and no
-// larger than gives every warp a page. Block i of the unit (forced blocks,
-// then the routed list) goes to warp i mod 8 CL of the cluster, and each warp
-// works out its own blocks from the list, so a CTA starts without a barrier.
+// One cluster of CL CTAs of four warps per (sequence, KV head): CL as large as
+// keeps every unit's cluster resident at once (four CTAs per SM), and no larger
+// than gives every warp a page. Block i of the unit (forced blocks, then the
+// routed list) goes to warp i mod 4 CL of the cluster, and each warp works out
+// its own blocks from the list, so a CTA starts without a barrier. (CTAs of
+// eight warps, two per SM: the same up to 296 units, where all are resident
+// either way; 43 against 41 us for 512 units of 108 pages, which then take two
+// rounds of CTAs.) Bound by instructions, about 390 a page, at 16 warps an SM:
+// 127 MB in 41 us.
 // hga_decode_pages.cuh has the arithmetic and the joining of the partials.
 #include <cooperative_groups.h>
 
@@ -26,12 +30,12 @@ namespace hga {
 
 namespace {
 
-using dec::kConsumers;
 using dec::kMaxCluster;
-constexpr int kPageThreads = kConsumers * 32;
+constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 4;  // at 120 registers a thread
 
-struct PagesSmem : dec::PageSmem {
-    int2 blk[kConsumers][kMaxBlocks / kConsumers];  // per warp: page (kSrcGathered: of the
+struct PagesSmem : dec::PageSmem<kWarps> {
+    int2 blk[kWarps][kMaxBlocks / kWarps];  // per warp: page (kSrcGathered: of the
                                                     // gathered buffer), first position
 };
 
@@ -52,7 +56,7 @@ __host__ __device__ __forceinline__ Forced forced_of(const Params& p) {
     return f;
 }
 
-__global__ void __launch_bounds__(kPageThreads, 2) attend_pages_kernel(
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) attend_pages_kernel(
     const __grid_constant__ dec::PageSource res, const __grid_constant__ dec::PageSource gat,
     const __grid_constant__ Params p, const __nv_bfloat16* __restrict__ q,
     const int32_t* __restrict__ sel, const int32_t* __restrict__ nsel,
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(kPageThreads, 2) attend_pages_kernel(
 
     // ---- this warp's blocks; the count and the first 32 entries in one round trip
     const Forced f = forced_of(p);
-    const int first = warp * CL + r, step = kConsumers * CL;
+    const int first = warp * CL + r, step = kWarps * CL;
     const int32_t* list = sel + bh * p.kg;
     auto entry = [&](int s) { return s >= 0 && s < p.kg ? list[s] : -1; };
     int s = first + step * lane - f.blocks;
@@ -123,13 +127,13 @@ __global__ void __launch_bounds__(kPageThreads, 2) attend_pages_kernel(
             return dec::page_at((page & kSrcGathered) ? gbase : rbase, page & ~kSrcGathered);
         },
         [&](int i) { return sm.blk[warp][i].y; }, acc);
-    dec::merge_pages(sm, cluster, p, acc, b, h, out);
+    dec::merge_pages<kWarps>(sm, cluster, p, acc, b, h, out);
 }
 
 cudaLaunchConfig_t config_of(int cl, int64_t units, cudaLaunchAttribute* attr, cudaStream_t st) {
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(cl, (unsigned)units, 1);
-    c.blockDim = dim3(kPageThreads);
+    c.blockDim = dim3(32 * kWarps);
     c.dynamicSmemBytes = sizeof(PagesSmem);
     c.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -142,13 +146,13 @@ cudaLaunchConfig_t config_of(int cl, int64_t units, cudaLaunchAttribute* attr, c
 }
 
 std::mutex g_pages_mu;
-// per device: clusters of each size resident at once (0 = not queried)
-int g_pages_active[kMaxDevicesPerProcess][kMaxCluster + 1] = {};
 
-// The largest cluster size, at most `most`, of which all units' are resident at once.
+// The largest cluster size, at most `most`, of which all units' are resident at
+// once. Per device, resident clusters of each size are asked for once.
 int cluster_size(int most, int64_t units, int dev) {
+    static int active_of[kMaxDevicesPerProcess][kMaxCluster + 1] = {};  // 0: not asked yet
     std::lock_guard<std::mutex> lock(g_pages_mu);
-    int* active = g_pages_active[dev];
+    int* active = active_of[dev];
     int cl = most;
     for (; cl > 1; --cl) {
         if (active[cl] == 0) {
@@ -190,8 +194,8 @@ cudaError_t launch_attend_pages(const Params& p, const void* q_rot, const KvSour
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t units = (int64_t)p.B * p.Hu;
     const int blocks = forced_of(p).blocks + p.kg;
-    int64_t most = 2 * sms / units;  // two CTAs per SM
-    if (most > (blocks + kConsumers - 1) / kConsumers) most = (blocks + kConsumers - 1) / kConsumers;
+    int64_t most = (int64_t)kCtasPerSm * sms / units;
+    if (most > (blocks + kWarps - 1) / kWarps) most = (blocks + kWarps - 1) / kWarps;
     most = most < 1 ? 1 : (most > kMaxCluster ? kMaxCluster : most);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t c = config_of(cluster_size((int)most, units, dev), units, attr, st);

@@ -99,7 +99,7 @@ struct StepTables {
 };
 
 template <int kKv>
-struct StepSmem : std::conditional_t<kKv == kKvE2m1, dec::PageSmem, StepRing>, StepTables {};
+struct StepSmem : std::conditional_t<kKv == kKvE2m1, dec::PageSmem<kConsumers>, StepRing>, StepTables {};
 
 __device__ __forceinline__ uint64_t rank_key(uint32_t key32, int idx) {
     return key32 ? ((uint64_t)key32 << 32) | (uint32_t)(0x7fffffff - idx) : 0ull;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_step_kernel(
                 },
                 [&](int i) { return sm.blk_pos[warp + kConsumers * i]; }, acc);
         }
-        dec::merge_pages(sm, cluster, p, acc, b, h, out);
+        dec::merge_pages<kConsumers>(sm, cluster, p, acc, b, h, out);
     } else {
         if (warp == kConsumers) {
             // lane 0 waits for free stages and issues the tile loads of resident
