@@ -11,6 +11,7 @@ libhga.so has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -121,12 +122,38 @@ def pair_axes(half: int, sections, interleaved: bool = False) -> list:
 def rope_axes(pair_axis, n_axes: int, inverse: bool = False) -> HgaRopeAxes:
     """hga_rope_axes from the axis of each pair (pair_axes makes such lists)."""
     pair_axis = [int(a) for a in pair_axis]
-    if len(pair_axis) > 64 or any(not -128 <= a < 128 for a in pair_axis):
+    if len(pair_axis) > 64 or not all(-128 <= a < 128 for a in pair_axis):
         raise ValueError("pair_axis: at most 64 entries of -1 .. n_axes - 1")
-    s = HgaRopeAxes(n_axes=int(n_axes), inverse=int(bool(inverse)))
-    for i in range(64):
-        s.pair_axis[i] = pair_axis[i] if i < len(pair_axis) else -1
-    return s
+    return HgaRopeAxes(n_axes=int(n_axes), inverse=int(bool(inverse)),
+                       pair_axis=(ctypes.c_int8 * 64)(*pair_axis, *[-1] * (64 - len(pair_axis))))
+
+
+class _Shapes:
+    """What calls of one configuration ask of their tensors."""
+
+    def __init__(self, c: HgaConfig):
+        if c.chunk_size < 1 or c.groups_per_chunk < 1:
+            raise HgaError(-8, "configuration")
+        B, H, L, d, nQC, R = (c.batch, c.n_kv_heads, c.seq_len, c.head_dim, c.n_qchunks,
+                              c.route_heads)
+        self.batch, self.kv_heads, self.d = B, H, d
+        self.dtype, self.kv_dtype = c.torch_dtype(), c.kv_torch_dtype()
+        self.store = c.kv_rows(B, H, rows=L)
+        self.res = (self.store if c.kv_layout == HGA_KV_FULL
+                    else c.kv_rows(B, H, rows=window_slots(c) * c.chunk_size))
+        self.gathered = c.kv_rows(B, H, nQC, rows=c.top_k_groups * c.group_size)
+        self.q = (B, c.q_len, c.n_q_heads, d)
+        self.sel, self.n_sel = (B, R, nQC, c.top_k_groups), (B, R, nQC)
+
+
+@functools.lru_cache(maxsize=256)
+def _shapes_of(fields: bytes) -> _Shapes:
+    return _Shapes(HgaConfig.from_buffer_copy(fields))
+
+
+def _shapes(cfg: HgaConfig) -> _Shapes:
+    """By the configuration's values, so that a decode loop works them out once."""
+    return _shapes_of(bytes(cfg))
 
 
 def _load():
@@ -211,9 +238,16 @@ def _stream(stream) -> int:
 
 def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=True,
          nullable=False) -> Optional[int]:
+    """Address of a tensor that has the type, shape, place and layout asked for."""
+    if t is None and nullable:
+        return None
+    # one pass for a tensor that is as it should be (a call's checks are most of
+    # its host time); what is wrong with another one, below
+    if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous()
+            and (not device or t.get_device() == torch._C._cuda_getDevice())):
+        return t.data_ptr()
     if t is None:
-        if nullable:
-            return None
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -224,7 +258,7 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=Tr
                          f"not on {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -250,16 +284,16 @@ def apply_rope_axes(cfg: HgaConfig, axes: HgaRopeAxes, positions: torch.Tensor, 
                     x_rot: torch.Tensor, n_outer: int, n_tokens: int, n_heads: int,
                     stream=None) -> None:
     """Rotate by positions [n_axes, n_batch, n_tokens] int32 (see hga_apply_rope_axes)."""
-    shape = (n_outer, n_tokens, n_heads, cfg.head_dim)
-    if x.numel() != n_outer * n_tokens * n_heads * cfg.head_dim:
-        raise ValueError(f"x must hold {shape} elements")
+    s = _shapes(cfg)
+    if x.numel() != n_outer * n_tokens * n_heads * s.d:
+        raise ValueError(f"x must hold {(n_outer, n_tokens, n_heads, s.d)} elements")
     if not isinstance(positions, torch.Tensor) or positions.dim() != 3:
         raise ValueError("positions must be a [n_axes, n_batch, n_tokens] tensor")
-    n_batch = int(positions.shape[1])
+    n_batch = positions.shape[1]
     _check(_lib.hga_apply_rope_axes(
         ctypes.byref(cfg), ctypes.byref(axes),
         _ptr(positions, "positions", torch.int32, (axes.n_axes, n_batch, n_tokens)),
-        _ptr(x, "x", cfg.torch_dtype()), _ptr(x_rot, "x_rot", cfg.torch_dtype(), x.shape),
+        _ptr(x, "x", s.dtype), _ptr(x_rot, "x_rot", s.dtype, x.shape),
         n_batch, n_outer, n_tokens, n_heads, _stream(stream)), "hga_apply_rope_axes")
 
 
@@ -283,34 +317,33 @@ def store_kv(cfg: HgaConfig, k, v, k_store, v_store, pos0: int, axes: Optional[H
              positions=None, stream=None) -> None:
     """Quantise k, v [B, Hkv, n, d] into rows [pos0, pos0 + n) of an E2M1 store;
     with axes the keys are rotated first (see hga_store_kv)."""
-    B, H, d = cfg.batch, cfg.n_kv_heads, cfg.head_dim
+    c = _shapes(cfg)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, Hkv, n, d] tensor")
-    n = int(k.shape[2])
-    dt, store = torch.bfloat16, cfg.kv_rows(B, H, rows=cfg.seq_len)
     if positions is not None and axes is None:
         raise ValueError("positions need axes")
+    n = k.shape[2]
+    rows = (c.batch, c.kv_heads, n, c.d)
     _check(_lib.hga_store_kv(
         ctypes.byref(cfg), ctypes.byref(axes) if axes is not None else None,
         _ptr(positions, "positions", torch.int32,
-             (axes.n_axes, B, n) if axes is not None else None, nullable=True),
-        _ptr(k, "k", dt, (B, H, n, d)), _ptr(v, "v", dt, (B, H, n, d)),
-        _ptr(k_store, "k_store", cfg.kv_torch_dtype(), store),
-        _ptr(v_store, "v_store", cfg.kv_torch_dtype(), store), int(pos0), n, _stream(stream)),
-        "hga_store_kv")
+             (axes.n_axes, c.batch, n) if axes is not None else None, nullable=True),
+        _ptr(k, "k", torch.bfloat16, rows), _ptr(v, "v", torch.bfloat16, rows),
+        _ptr(k_store, "k_store", c.kv_dtype, c.store), _ptr(v_store, "v_store", c.kv_dtype, c.store),
+        int(pos0), n, _stream(stream)), "hga_store_kv")
 
 
 def load_kv(cfg: HgaConfig, k_store, v_store, k, v, pos0: int, stream=None) -> None:
     """Rows [pos0, pos0 + n) of an E2M1 store as bf16 k, v [B, Hkv, n, d]."""
-    B, H, d = cfg.batch, cfg.n_kv_heads, cfg.head_dim
+    c = _shapes(cfg)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, Hkv, n, d] tensor")
-    n = int(k.shape[2])
-    dt, store = torch.bfloat16, cfg.kv_rows(B, H, rows=cfg.seq_len)
+    n = k.shape[2]
+    rows = (c.batch, c.kv_heads, n, c.d)
     _check(_lib.hga_load_kv(
-        ctypes.byref(cfg), _ptr(k_store, "k_store", cfg.kv_torch_dtype(), store),
-        _ptr(v_store, "v_store", cfg.kv_torch_dtype(), store), _ptr(k, "k", dt, (B, H, n, d)),
-        _ptr(v, "v", dt, (B, H, n, d)), int(pos0), n, _stream(stream)), "hga_load_kv")
+        ctypes.byref(cfg), _ptr(k_store, "k_store", c.kv_dtype, c.store),
+        _ptr(v_store, "v_store", c.kv_dtype, c.store), _ptr(k, "k", torch.bfloat16, rows),
+        _ptr(v, "v", torch.bfloat16, rows), int(pos0), n, _stream(stream)), "hga_load_kv")
 
 
 def build_summaries(cfg: HgaConfig, k_raw, chunk_sum, group_sum, k_rot=None, chunk_begin=0,
@@ -491,20 +524,15 @@ def window_slots(cfg: HgaConfig) -> int:
 
 def attend(cfg: HgaConfig, q_rot, k_res, v_res, sel_groups, n_sel_groups, out, k_gat=None,
            v_gat=None, stream=None) -> None:
-    B, H, L, d, nQC = cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_qchunks
-    dt, kvt = cfg.torch_dtype(), cfg.kv_torch_dtype()
-    res_len = L if cfg.kv_layout == HGA_KV_FULL else window_slots(cfg) * cfg.chunk_size
-    gat_shape = cfg.kv_rows(B, H, nQC, rows=cfg.top_k_groups * cfg.group_size)
-    res_shape = cfg.kv_rows(B, H, rows=res_len)
-    q_shape = (B, cfg.q_len, cfg.n_q_heads, d)
+    c = _shapes(cfg)
     _check(_lib.hga_attend(
-        ctypes.byref(cfg), _ptr(q_rot, "q_rot", dt, q_shape),
-        _ptr(k_res, "k_res", kvt, res_shape), _ptr(v_res, "v_res", kvt, res_shape),
-        _ptr(k_gat, "k_gat", kvt, gat_shape, nullable=True),
-        _ptr(v_gat, "v_gat", kvt, gat_shape, nullable=True),
-        _ptr(sel_groups, "sel_groups", torch.int32, (B, cfg.route_heads, nQC, cfg.top_k_groups)),
-        _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, cfg.route_heads, nQC)),
-        _ptr(out, "out", dt, q_shape), _stream(stream)), "hga_attend")
+        ctypes.byref(cfg), _ptr(q_rot, "q_rot", c.dtype, c.q),
+        _ptr(k_res, "k_res", c.kv_dtype, c.res), _ptr(v_res, "v_res", c.kv_dtype, c.res),
+        _ptr(k_gat, "k_gat", c.kv_dtype, c.gathered, nullable=True),
+        _ptr(v_gat, "v_gat", c.kv_dtype, c.gathered, nullable=True),
+        _ptr(sel_groups, "sel_groups", torch.int32, c.sel),
+        _ptr(n_sel_groups, "n_sel_groups", torch.int32, c.n_sel), _ptr(out, "out", c.dtype, c.q),
+        _stream(stream)), "hga_attend")
 
 
 def get_device_error(stream=None) -> int:
