@@ -23,49 +23,62 @@ using bf = __nv_bfloat16;
 
 constexpr int kStoreThreads = 256;
 
-// Division of row numbers by the tokens per unit. 32 bits (numbers below 2^31):
-// by multiplication, n / d = (mulhi(n, m) + n) >> s with s = ceil(log2 d) and m =
-// floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery).
-struct Div32 {
-    using I = uint32_t;
-    uint32_t d, m, s;
-    explicit Div32(int64_t tokens) : d((uint32_t)tokens), s(0) {
+// One launch's rows, those of `units` units from u0 on, d tokens each, numbered
+// unit by unit; row / d by multiplication, (mulhi(row, m) + row) >> s with s =
+// ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery),
+// right for rows below 2^31.
+constexpr int64_t kRowsPerLaunch = 1 << 22;  // 16 lanes each and a grid past them fit 31 bits
+static_assert((int64_t)kMaxChunks * 8 * kGroupRows <= kRowsPerLaunch, "a unit fits one launch");
+
+struct Rows {
+    uint32_t d, m, s, n;  // n: rows
+    int64_t u0;
+    Rows(int64_t u0_, int64_t units, int64_t tokens)
+        : d((uint32_t)tokens), s(0), n((uint32_t)(units * tokens)), u0(u0_) {
         while (((uint64_t)1 << s) < d) ++s;
         m = (uint32_t)(((uint64_t)1 << 32) * (((uint64_t)1 << s) - d) / d + 1);
     }
-    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-        return (__umulhi(n, m) + n) >> s;
+    __device__ __forceinline__ void find(uint32_t row, int64_t& unit, int& token) const {
+        const uint32_t u = (__umulhi(row, m) + row) >> s;
+        unit = u0 + u;
+        token = (int)(row - u * d);
     }
 };
-struct Div64 {
-    using I = uint64_t;
-    uint64_t d;
-    explicit Div64(int64_t tokens) : d((uint64_t)tokens) {}
-    __device__ __forceinline__ uint64_t operator()(uint64_t n) const { return n / d; }
-};
 
-// Where a row of a call's token t of unit bh starts in a store: its page; *row:
-// within it.
+// f(Rows) for each launch of a call.
+template <typename F>
+cudaError_t each_launch(int64_t units, int64_t n_tokens, F f) {
+    const int64_t per = kRowsPerLaunch / n_tokens;
+    for (int64_t u = 0; u < units; u += per) {
+        f(Rows(u, units - u < per ? units - u : per, n_tokens));
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// Where position `at` of unit bh is in a store: its page; *row: within it.
 __device__ __forceinline__ int64_t page_of(const Params& p, int64_t bh, int at, int* row) {
     *row = at % kGroupRows;
     return bh * p.kv_slab + (int64_t)(at / kGroupRows) * kE2m1Page;
 }
 
 // Rows as they are. Item = (row, block): row * 8 + block, so eight lanes hold
-// the eight blocks of a row; its scales are written four bytes at a time. I: an
-// unsigned type that holds the item count and a grid more.
-template <typename Div, typename I = typename Div::I>
+// the eight blocks of a row; its scales are written four bytes at a time.
 __device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8_t* store, float ts,
-                                           int pos0, const Div& unit, I n_rows) {
+                                           int pos0, const Rows& rows) {
     const e2m1::TensorScale tensor = e2m1::tensor_scale(ts);
     const int blk = threadIdx.x & 7;
-    const I n_items = n_rows * 8;
+    const uint32_t n_items = rows.n * 8;
     // whole warps stay to the end: their lanes exchange scales
-    for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; (it & ~(I)31) < n_items;
-         it += (I)gridDim.x * kStoreThreads) {
+    for (uint32_t it = blockIdx.x * kStoreThreads + threadIdx.x; (it & ~31u) < n_items;
+         it += gridDim.x * kStoreThreads) {
         const bool ok = it < n_items;
-        const I row = ok ? it >> 3 : 0, bh = unit(row), t = row - bh * unit.d;
-        const uint4* src16 = reinterpret_cast<const uint4*>(src + (int64_t)row * 128 + kBlock * blk);
+        int64_t bh;
+        int t;
+        rows.find(ok ? it >> 3 : 0, bh, t);
+        const uint4* src16 =
+            reinterpret_cast<const uint4*>(src + (bh * rows.d + t) * 128 + kBlock * blk);
         const uint4 r0 = src16[0], r1 = src16[1];
         const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
         // the largest magnitude as bits; infinities and NaN are the largest
@@ -78,7 +91,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8
         bf16x8_to_f32(r0, x);
         bf16x8_to_f32(r1, x + 8);
         int pr;
-        uint8_t* pg = store + page_of(p, bh, pos0 + (int)t, &pr);
+        uint8_t* pg = store + page_of(p, bh, pos0 + t, &pr);
         if (ok)
             *reinterpret_cast<uint2*>(pg + e2m1::code_at(pr, kBlock * blk)) =
                 make_uint2(e2m1::codes_of(x, sc), e2m1::codes_of(x + 8, sc));
@@ -91,13 +104,12 @@ __device__ __forceinline__ void store_rows(const Params& p, const bf* src, uint8
 
 // Keys rotated on the way. 16 lanes a row, each with 4 rotary pairs: dims
 // 4l .. + 3 and 64 + 4l .. + 3. Item = (row, lane): row * 16 + lane.
-template <typename Div, typename I = typename Div::I>
 __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am,
                                               const int32_t* pos, const bf* k, uint8_t* ks,
-                                              int pos0, const Div& unit, I n_rows) {
+                                              int pos0, const Rows& rows) {
     const e2m1::TensorScale tensor = e2m1::tensor_scale(p.k_scale);
     const int l = threadIdx.x & 15;
-    const I n_items = n_rows * 16;
+    const uint32_t n_items = rows.n * 16;
     // this lane's pairs, read once (the constant cache serves one index at a time)
     double freq[4];
     int axis[4];
@@ -106,12 +118,15 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
         freq[e] = p.inv_freq[4 * l + e];
         axis[e] = am.axis[4 * l + e];
     }
-    for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; (it & ~(I)31) < n_items;
-         it += (I)gridDim.x * kStoreThreads) {
+    for (uint32_t it = blockIdx.x * kStoreThreads + threadIdx.x; (it & ~31u) < n_items;
+         it += gridDim.x * kStoreThreads) {
         const bool ok = it < n_items;
-        const I row = ok ? it >> 4 : 0, bh = unit(row), t = row - bh * unit.d;
-        const int at = pos0 + (int)t;
-        const uint2* src8 = reinterpret_cast<const uint2*>(k + (int64_t)row * 128 + 4 * l);
+        int64_t bh;
+        int t;
+        rows.find(ok ? it >> 4 : 0, bh, t);
+        const int at = pos0 + t;
+        const uint2* src8 =
+            reinterpret_cast<const uint2*>(k + (bh * rows.d + t) * 128 + 4 * l);
         const uint2 lo = src8[0], hi = src8[16];
         const uint32_t wl[2] = {lo.x, lo.y}, wh[2] = {hi.x, hi.y};
         float x[2][4];  // dims 4l .. and 64 + 4l ..
@@ -123,7 +138,8 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
             x[1][e] = b;
             if (axis[e] >= 0) {
                 const double at_axis =
-                    pos ? (double)pos[((int64_t)axis[e] * p.B + bh / p.Hkv) * unit.d + t] : (double)at;
+                    pos ? (double)pos[(axis[e] * (int64_t)p.B + bh / p.Hkv) * rows.d + t]
+                        : (double)at;
                 double c, sn;
                 turn_cs64(at_axis, freq[e], c, sn);
                 x[0][e] = (float)((double)a * c - (double)b * sn);
@@ -155,51 +171,54 @@ __device__ __forceinline__ void store_rotated(const Params& p, const AxisMap& am
 }
 
 // grid.y = 0: keys, 1: values.
-template <typename Div, bool kRotate>
+template <bool kRotate>
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(
     const __grid_constant__ Params p, const __grid_constant__ AxisMap am,
     const int32_t* __restrict__ pos, const bf* __restrict__ k, const bf* __restrict__ v,
-    uint8_t* __restrict__ ks, uint8_t* __restrict__ vs, int pos0, Div unit,
-    typename Div::I n_rows) {
+    uint8_t* __restrict__ ks, uint8_t* __restrict__ vs, int pos0, Rows rows) {
     if (blockIdx.y == 1)
-        store_rows(p, v, vs, p.v_scale, pos0, unit, n_rows);
+        store_rows(p, v, vs, p.v_scale, pos0, rows);
     else if (kRotate)
-        store_rotated(p, am, pos, k, ks, pos0, unit, n_rows);
+        store_rotated(p, am, pos, k, ks, pos0, rows);
     else
-        store_rows(p, k, ks, p.k_scale, pos0, unit, n_rows);
+        store_rows(p, k, ks, p.k_scale, pos0, rows);
 }
 
 // grid.y = 0: keys, 1: values. Item = (row, 8 dims): row * 16 + piece; a
 // thread has kLoadItems of them in flight, a grid apart.
 constexpr int kLoadItems = 4;
 
-template <typename Div, typename I = typename Div::I>
 __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
     const __grid_constant__ Params p, const uint8_t* __restrict__ ks,
     const uint8_t* __restrict__ vs, bf* __restrict__ k, bf* __restrict__ v, int pos0,
-    Div unit, I n_items) {
+    Rows rows) {
     const uint8_t* store = blockIdx.y ? vs : ks;
     bf* dst = blockIdx.y ? v : k;
     const float ts = blockIdx.y ? p.v_scale : p.k_scale;
     const int pc = threadIdx.x & 15;
-    const I step = (I)gridDim.x * kStoreThreads;
-    for (I it = (I)blockIdx.x * kStoreThreads + threadIdx.x; it < n_items; it += step * kLoadItems) {
+    const uint32_t n_items = rows.n * 16, step = gridDim.x * kStoreThreads;
+    for (uint32_t it = blockIdx.x * kStoreThreads + threadIdx.x; it < n_items;
+         it += step * kLoadItems) {
+        int64_t dst_row[kLoadItems];
         uint32_t w[kLoadItems];
         uint8_t sc[kLoadItems];
 #pragma unroll
         for (int i = 0; i < kLoadItems; ++i) {
-            const I x = it + step * i;
+            const uint32_t x = it + step * i;
             if (x < n_items) {
-                const I row = x >> 4, bh = unit(row), t = row - bh * unit.d;
+                int64_t bh;
+                int t;
+                rows.find(x >> 4, bh, t);
+                dst_row[i] = bh * rows.d + t;
                 int pr;
-                const uint8_t* pg = store + page_of(p, bh, pos0 + (int)t, &pr);
+                const uint8_t* pg = store + page_of(p, bh, pos0 + t, &pr);
                 w[i] = *reinterpret_cast<const uint32_t*>(pg + e2m1::code_at(pr, 8 * pc));
                 sc[i] = pg[e2m1::scale_at(pr, pc >> 1)];
             }
         }
 #pragma unroll
         for (int i = 0; i < kLoadItems; ++i) {
-            const I x = it + step * i;
+            const uint32_t x = it + step * i;
             if (x < n_items) {
                 const uint32_t s2 = e2m1::scales_to_f16x2((uint16_t)(sc[i] * 0x101u));
                 uint32_t f[4];
@@ -212,7 +231,7 @@ __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
                     o[2 * e] = r.x * ts;
                     o[2 * e + 1] = r.y * ts;
                 }
-                *reinterpret_cast<uint4*>(dst + (int64_t)(x >> 4) * 128 + 8 * pc) = f32x8_to_bf16(o);
+                *reinterpret_cast<uint4*>(dst + dst_row[i] * 128 + 8 * pc) = f32x8_to_bf16(o);
             }
         }
     }
@@ -224,49 +243,27 @@ unsigned grid_of(int64_t items) {
     return (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16);
 }
 
-// f(the division for a call's row numbers): 32 bits where items and the grids'
-// strides past them fit.
-template <typename F>
-void with_division(int64_t items, int64_t n_tokens, F f) {
-    if (items < (int64_t)1 << 30)
-        f(Div32(n_tokens));
-    else
-        f(Div64(n_tokens));
-}
-
 }  // namespace
 
 cudaError_t launch_store_kv(const Params& p, const AxisMap& am, const int32_t* positions,
                             const void* k, const void* v, void* k_store, void* v_store,
                             int64_t pos0, int64_t n_tokens, cudaStream_t st) {
-    const int64_t rows = (int64_t)p.B * p.Hkv * n_tokens;
     const bool rotate = am.n_axes > 0;
-    with_division(rows * 16, n_tokens, [&](auto unit) {
-        using Div = decltype(unit);
-        auto run = [&](auto* kernel, int lanes) {
-            kernel<<<dim3(grid_of(rows * lanes), 2), kStoreThreads, 0, st>>>(
-                p, am, positions, (const bf*)k, (const bf*)v, (uint8_t*)k_store, (uint8_t*)v_store,
-                (int)pos0, unit, (typename Div::I)rows);
-        };
-        if (rotate)
-            run(store_kv_kernel<Div, true>, 16);
-        else
-            run(store_kv_kernel<Div, false>, 8);
+    auto* kernel = rotate ? store_kv_kernel<true> : store_kv_kernel<false>;
+    return each_launch((int64_t)p.B * p.Hkv, n_tokens, [&](const Rows& rows) {
+        kernel<<<dim3(grid_of((int64_t)rows.n * (rotate ? 16 : 8)), 2), kStoreThreads, 0, st>>>(
+            p, am, positions, (const bf*)k, (const bf*)v, (uint8_t*)k_store, (uint8_t*)v_store,
+            (int)pos0, rows);
     });
-    return cudaGetLastError();
 }
 
 cudaError_t launch_load_kv(const Params& p, const void* k_store, const void* v_store, void* k,
                            void* v, int64_t pos0, int64_t n_tokens, cudaStream_t st) {
-    const int64_t rows = (int64_t)p.B * p.Hkv * n_tokens;
-    with_division(rows * 16, n_tokens, [&](auto unit) {
-        using Div = decltype(unit);
-        const dim3 grid(grid_of((rows * 16 + kLoadItems - 1) / kLoadItems), 2);
-        load_kv_kernel<Div><<<grid, kStoreThreads, 0, st>>>(
-            p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, (int)pos0, unit,
-            (typename Div::I)(rows * 16));
+    return each_launch((int64_t)p.B * p.Hkv, n_tokens, [&](const Rows& rows) {
+        const int64_t threads = ((int64_t)rows.n * 16 + kLoadItems - 1) / kLoadItems;
+        load_kv_kernel<<<dim3(grid_of(threads), 2), kStoreThreads, 0, st>>>(
+            p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, (int)pos0, rows);
     });
-    return cudaGetLastError();
 }
 
 }  // namespace hga

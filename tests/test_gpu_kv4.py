@@ -563,3 +563,192 @@ def test_append_axes_bf16():
     assert torch.equal(cs[:, :, :1], cs1[:, :, :1]) and torch.equal(gs[:, :, :4], gs1[:, :, :4])
     d = (kr.float() - kr1.float()).abs()
     assert bool((d <= 2 * R.BF16 * kr1.float().abs() + 2.0 ** -18).all())
+
+
+# ------------------------------------------------- the other ways to a result
+STEPS = [dict(seq_len=1024), dict(seq_len=999, n_q_heads=10), dict(seq_len=1000, q_begin=700),
+         dict(seq_len=2000, summary_type=1), dict(seq_len=777, routing=1),
+         dict(seq_len=1100, n_q_heads=24), dict(seq_len=3000, top_k_chunks=100, n_local=1),
+         dict(seq_len=40), dict(seq_len=640, chunk_size=128, groups_per_chunk=8)]
+
+
+@pytest.mark.parametrize("kw", STEPS, ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_decode_step(kw):
+    """hga_decode_step over the 4-bit store: the selections of hga_route, and attention
+    over them; where the cache may lie in host memory, the tiered step the same."""
+    from long_context_rope_b200 import hga, pipeline
+    kw = dict(dict(batch=2, n_kv_heads=2, n_q_heads=16, q_begin=kw["seq_len"] - 1), **kw)
+    cfg = _cfg4(hga, **kw)
+    q, kp, vp, _, _, _, _ = _attend_case(hga, cfg, 80, count=0)
+    qd, kd, vd = q.cuda(), kp.cuda(), vp.cuda()
+    cs, gs = pipeline.alloc_summaries(cfg)
+    g = torch.Generator(device="cuda").manual_seed(81)
+    cs.copy_(torch.randn(cs.shape, device="cuda", generator=g))
+    gs.copy_(torch.randn(gs.shape, device="cuda", generator=g))
+    rb0, rb = pipeline.alloc_route(cfg), pipeline.alloc_route(cfg)
+    pipeline.route(cfg, qd, cs, gs, rb0)
+    kv = [torch.nan_to_num(R.values(p, ts)) for p, ts in ((kp, cfg.k_scale), (vp, cfg.v_scale))]
+    want, tol = R.attend(cfg, q, *kv, rb0.sel_groups.cpu(), rb0.n_sel_groups.cpu())
+
+    def check(step, name):
+        out = torch.full(q.shape, float("nan"), dtype=BF, device="cuda")
+        try:
+            step(out)
+        except hga.HgaError as e:   # 12 heads a KV head, 100 chunks: separate calls only
+            assert name == "tiered" and "UNSUPPORTED" in str(e)
+            assert cfg.n_q_heads == 24 or cfg.top_k_chunks == 100
+            return
+        _clean(hga)
+        assert torch.equal(rb.sel_groups, rb0.sel_groups) and torch.equal(rb.sel_chunks, rb0.sel_chunks)
+        assert torch.equal(rb.qbar, rb0.qbar)
+        _check(out, want, tol)
+    check(lambda out: pipeline.decode(cfg, qd, cs, gs, kd, vd, rb, out), "step")
+    if cfg.q_begin == cfg.seq_len - 1:
+        cfg_w = cfg.copy(kv_layout=hga.HGA_KV_WINDOWS)
+        rows = hga.window_slots(cfg) * cfg.chunk_size
+        win = [torch.zeros(cfg.kv_rows(2, 2, rows=rows), dtype=torch.uint8, device="cuda") for _ in "kv"]
+        kh, vh = kp.pin_memory(), vp.pin_memory()
+        pipeline.fill_windows(cfg, kh, vh, *win)
+        check(lambda out: pipeline.decode_tiered(cfg_w, qd, cs, gs, *win, kh, vh, rb, out), "tiered")
+
+
+MORE = [dict(seq_len=200, chunk_size=16, groups_per_chunk=1), dict(seq_len=500, chunk_size=128,
+                                                                    groups_per_chunk=8),
+        dict(seq_len=150, n_q_heads=16), dict(seq_len=150, n_q_heads=7), dict(seq_len=70, n_q_heads=128),
+        dict(seq_len=70, n_q_heads=130), dict(seq_len=900, top_k_groups=400, n_local=1)]
+
+
+@pytest.mark.parametrize("kw", MORE, ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+@pytest.mark.parametrize("gathered", [False, True])
+def test_attend_more_shapes(kw, gathered):
+    """Chunks of one group and of eight, many heads, long lists; each as a prefill of the
+    last 40 tokens and as a decode step; from the store and from gathered buffers."""
+    from long_context_rope_b200 import hga, pipeline
+    for n in (40, 1):
+        cfg = _cfg4(hga, **dict(kw, q_begin=kw["seq_len"] - n, q_len=n))
+        q, kp, vp, sel, cnt, want, tol = _attend_case(hga, cfg, 90)
+        qd, kd, vd, sd, nd = (t.cuda() for t in (q, kp, vp, sel, cnt))
+        gat = (None, None)
+        if gathered:
+            gat = pipeline.alloc_gathered(cfg)
+            hga.gather_kv(cfg, kd, vd, False, sd, nd, *gat)
+        out = torch.full(q.shape, float("nan"), dtype=BF, device="cuda")
+        hga.attend(cfg, qd, kd, vd, sd, nd, out, k_gat=gat[0], v_gat=gat[1])
+        again = torch.empty_like(out)
+        hga.attend(cfg, qd, kd, vd, sd, nd, again, k_gat=gat[0], v_gat=gat[1])
+        _clean(hga)
+        _check(out, want, tol)
+        assert torch.equal(out, again)   # no sum depends on the order of arrival
+
+
+def test_attend_per_query_head():
+    """Lists of a query head's own, in one call and on two streams at once."""
+    from long_context_rope_b200 import hga
+    cases = []
+    for seed in (100, 101):
+        cfg = _cfg4(hga, seq_len=1500, q_begin=1499, batch=2, n_kv_heads=2, n_q_heads=8,
+                    routing=hga.HGA_ROUTE_PER_Q_HEAD)
+        cases.append((cfg, _attend_case(hga, cfg, seed)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [[t.cuda() for t in c[:5]] for _, c in cases]
+    outs = [torch.full(c[0].shape, float("nan"), dtype=BF, device="cuda") for _, c in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (cfg, _), st, a, out in zip(cases, streams, args, outs):
+            hga.attend(cfg, *a, out, stream=st)
+    _clean(hga)
+    for (_, c), out in zip(cases, outs):
+        _check(out, c[5], c[6])
+
+
+def test_prefill_wait_limit():
+    """A prefill whose waits may last a nanosecond ends, with or without an error, and the
+    next one is right."""
+    from long_context_rope_b200 import hga
+    cfg = _cfg4(hga, seq_len=512, q_len=512)
+    c = _attend_case(hga, cfg, 110)
+    args = [t.cuda() for t in c[:5]]
+    out = torch.empty_like(args[0])
+    hga.set_wait_limit_ns(1)
+    try:
+        hga.attend(cfg, *args, out)
+        torch.cuda.synchronize()
+        hga.get_device_error()
+    finally:
+        hga.set_wait_limit_ns(0)
+    hga.attend(cfg, *args, out)
+    _clean(hga)
+    _check(out, c[5], c[6])
+
+
+def test_offsets_past_32_bits():
+    """A store of 4.8 GB per tensor (rows, pages and bytes past 2^31 and 2^32): the last
+    tokens written, read back and attended to as in a short store."""
+    from long_context_rope_b200 import hga
+    L, n = 1 << 20, 512
+    cfg = _cfg4(hga, batch=8, n_kv_heads=8, n_q_heads=16, seq_len=L, q_begin=L - 1, n_sink=0)
+    short = cfg.copy(seq_len=n, q_begin=n - 1)
+    k, v = _rows((8, 8, n, 128), 120).cuda(), _rows((8, 8, n, 128), 121).cuda()
+    q = _rows((8, 1, 16, 128), 122).cuda()
+    sel, cnt = R.lists(short, 8, 123)
+    outs, loads = [], []
+    for c in (cfg, short):
+        shift = c.seq_len - n
+        ks = torch.zeros(c.kv_rows(8, 8, rows=c.seq_len), dtype=torch.uint8, device="cuda")
+        vs = torch.zeros_like(ks)
+        hga.store_kv(c, k, v, ks, vs, shift, axes=hga.rope_axes([0, 1] * 32, 2),
+                     positions=torch.arange(2 * 8 * n, device="cuda", dtype=torch.int32).view(2, 8, n))
+        ko, vo, out = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+        hga.load_kv(c, ks, vs, ko, vo, shift)
+        moved = torch.where(sel >= 0, sel + shift // 16, sel).cuda()
+        hga.attend(c, q, ks, vs, moved, cnt.cuda(), out)
+        _clean(hga)
+        assert not ks[:, :, :shift // 16].any() and not vs[:, :, :shift // 16].any()
+        outs.append(out)
+        loads.append((ko, vo))
+        del ks, vs
+    assert torch.equal(*outs) and torch.equal(loads[0][0], loads[1][0])
+    assert torch.equal(loads[0][1], loads[1][1])
+
+
+def test_large_calls():
+    """More rows than one launch of the store takes, and a rotation of more than 2^31
+    elements: as the same work in parts."""
+    from long_context_rope_b200 import hga
+    n = 70000
+    cfg = _cfg4(hga, batch=8, n_kv_heads=8, n_q_heads=8, seq_len=n)
+    k = torch.randn(8, 8, n, 128, device="cuda", dtype=BF)
+    axes = hga.rope_axes([0] * 64, 1)
+    st = [torch.zeros(cfg.kv_rows(8, 8, rows=n), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    hga.store_kv(cfg, k, k, st[0], st[1], 0, axes=axes)
+    for a, b in ((0, 33333), (33333, n)):
+        part = k[:, :, a:b].contiguous()
+        hga.store_kv(cfg, part, part, st[2], st[3], a, axes=axes)
+    assert torch.equal(st[0], st[2]) and torch.equal(st[1], st[3])
+    o = [torch.empty_like(k) for _ in range(2)]
+    hga.load_kv(cfg, st[0], st[1], *o, 0)
+    part = torch.empty(8, 8, 1234, 128, device="cuda", dtype=BF), torch.empty(8, 8, 1234, 128, device="cuda",
+                                                                             dtype=BF)
+    hga.load_kv(cfg, st[0], st[1], *part, n - 1234)
+    assert torch.equal(o[0][:, :, n - 1234:], part[0]) and torch.equal(o[1][:, :, n - 1234:], part[1])
+    del o, part, st, k
+    T = (1 << 18) + 3
+    x = torch.randn(1, T, 64, 128, device="cuda", dtype=BF)
+    pos = torch.randint(0, 1 << 20, (2, 1, T), device="cuda", dtype=torch.int32)
+    axes = hga.rope_axes([0, 1] * 32, 2)
+    last = x[:, -5:].clone()
+    hga.apply_rope_axes(cfg, axes, pos, x, x, 1, T, 64)
+    y = torch.empty_like(last)
+    hga.apply_rope_axes(cfg, axes, pos[:, :, -5:].contiguous(), last, y, 1, 5, 64)
+    _clean(hga)
+    assert torch.equal(x[:, -5:], y)
+
+
+def test_other_device_is_refused():
+    from long_context_rope_b200 import hga
+    cfg = _cfg4(hga, seq_len=16, q_begin=15)
+    k = torch.zeros(1, 1, 16, 128, dtype=BF)
+    st = torch.zeros(1, 1, 1, 1152, dtype=torch.uint8, device="cuda")
+    for bad in (k, k.cuda().transpose(2, 3).contiguous().transpose(2, 3), k.cuda().float()):
+        with pytest.raises(ValueError):
+            hga.store_kv(cfg, bad, k.cuda(), st, st, 0)
