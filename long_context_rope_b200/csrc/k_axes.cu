@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "hga_kernels.h"
+#include "hga_ptx.cuh"
 #include "hga_turn.cuh"
 #include "hga_vec.cuh"
 
@@ -157,8 +158,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_axes_kernel(
 // chunk's angles: cos and sin of every token and pair, made once in shared
 // memory. Warp g owns group g: lane (q, u) the V pairs u*V .. of its tokens
 // q*R .. q*R + R - 1 (R = L/2 tokens for L lanes a row), so a warp's loads are
-// whole rows, and a group's sums need only shuffles over q. The chunk's sums go
-// over the groups in order. Mean positions are sums of integers, exact to
+// whole rows, and a group's sums need only shuffles over q. The sums of all heads
+// wait in shared memory for the end, where all threads turn them into means (a
+// barrier and a tail per head took two thirds of a head's time). The chunk's sums
+// go over the groups in order. Mean positions are sums of integers, exact to
 // double rounding.
 //
 // In the tables, 16-byte piece j of a row sits at j ^ (j >> 3), so that the
@@ -176,17 +179,17 @@ struct SumShape {
 };
 
 template <typename T, typename S, int D>
-__global__ void __launch_bounds__(256) summaries_axes_kernel(
+__global__ void __maxnreg__(112) summaries_axes_kernel(
     const __grid_constant__ Params p, const __grid_constant__ AxisMap am,
     const int32_t* __restrict__ pos, const T* __restrict__ k_raw, S* __restrict__ cs,
     S* __restrict__ gs, T* __restrict__ k_rot, int chunk_begin, int hp) {
     using Sh = SumShape<T, D>;
     constexpr int V = Sh::V, half = Sh::kHalf, L = Sh::L, R = Sh::R;
-    extern __shared__ __align__(16) float s_table[];      // cos of C x half, then sin
+    // cos of C x half, then sin; cos and sin of the mean angles of G groups and the
+    // chunk; per head the groups' sums, G x D (summaries_smem)
+    extern __shared__ __align__(16) float s_table[];
     __shared__ int s_pos[HGA_MAX_AXES][8 * kGroupRows];   // groups_per_chunk <= 8
     __shared__ int64_t s_psum[HGA_MAX_AXES][8];
-    __shared__ alignas(16) float s_mc[9][half], s_ms[9][half];  // mean angles: groups, chunk
-    __shared__ alignas(16) float s_sum[2][8][D];           // per head parity: the groups' sums
     const int G = p.G, tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
     const int u = lane & (L - 1), q = lane / L;
     const int ch = chunk_begin + blockIdx.x;
@@ -196,7 +199,10 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
     const int h0 = blockIdx.z * hp, h1 = h0 + hp < p.Hkv ? h0 + hp : p.Hkv;
     const int row0 = kGroupRows * g + R * q;
     float* tc = s_table;
-    float* ts = s_table + p.C * half;
+    float* ts = tc + p.C * half;
+    float* s_mc = ts + p.C * half;
+    float* s_ms = s_mc + (G + 1) * half;
+    float* s_sum = s_ms + (G + 1) * half;
 
     typename Vec<T>::Raw raw_a[R], raw_b[R];
     auto load_rows = [&](int h) {
@@ -240,8 +246,10 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
                     for (int r = tid / half; r < n_rows; r += per)
                         turn_cs((double)s_pos[ax][r], freq, tc[table_at(r, pair, half)],
                                 ts[table_at(r, pair, half)]);
-                if (ax >= 0 && low)
-                    for (int i = tid / half; i <= G; i += per) {
+                for (int i = tid / half; i <= G; i += per) {
+                    // a high pair, or one on no axis, takes no part
+                    float c = kNoTurn, sn = 0.f;
+                    if (ax >= 0 && low) {
                         int64_t sum = 0;
                         int n = n_rows;
                         if (i < G) {
@@ -250,20 +258,21 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
                         } else {
                             for (int y = 0; y < G; ++y) sum += s_psum[ax][y];
                         }
-                        turn_cs((double)sum / (double)n, freq, s_mc[i < G ? i : 8][pair],
-                                s_ms[i < G ? i : 8][pair]);
+                        turn_cs((double)sum / (double)n, freq, c, sn);
                     }
+                    s_mc[i * half + pair] = c;
+                    s_ms[i * half + pair] = sn;
+                }
             }
         }
     }
-    // bit e: pair u*V + e is rotated; token by token in the sums; by the mean angle
-    unsigned turn = 0, each = 0, mean = 0;
+    // bit e: pair u*V + e is rotated; token by token in the sums too
+    unsigned turn = 0, each = 0;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         const bool on = am.axis[u * V + e] >= 0, low = u * V + e >= p.F;
         turn |= (on && (!low || k_rot != nullptr) ? 1u : 0u) << e;
         each |= (on && !low ? 1u : 0u) << e;
-        mean |= (on && low ? 1u : 0u) << e;
     }
     // the whole warp's pairs are rotated token by token (the rotated keys are wanted)
     const bool all = __all_sync(0xffffffffu, turn == (1u << V) - 1u) != 0;
@@ -288,18 +297,30 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
                     *reinterpret_cast<float4*>(sn + e) = *reinterpret_cast<const float4*>(ts + at);
                 }
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const bool in = (each >> e) & 1u;
-                    float ra = a[e] * c[e] - bb[e] * sn[e], rb = a[e] * sn[e] + bb[e] * c[e];
+                for (int e = 0; e < V; e += 2) {
+                    // two pairs at a time
+                    const float2 a2 = {a[e], a[e + 1]}, b2 = {bb[e], bb[e + 1]};
+                    const float2 c2 = {c[e], c[e + 1]}, s2 = {sn[e], sn[e + 1]};
+                    float2 ra = ptx::sub2(ptx::mul2(a2, c2), ptx::mul2(b2, s2));
+                    float2 rb = ptx::fma2(a2, s2, ptx::mul2(b2, c2));
                     if (!all) {
-                        const bool on = (turn >> e) & 1u;
-                        ra = on ? ra : a[e];
-                        rb = on ? rb : bb[e];
+                        const bool on0 = (turn >> e) & 1u, on1 = (turn >> (e + 1)) & 1u;
+                        ra = {on0 ? ra.x : a2.x, on1 ? ra.y : a2.y};
+                        rb = {on0 ? rb.x : b2.x, on1 ? rb.y : b2.y};
                     }
-                    acc0[e] += in ? ra : a[e];
-                    acc1[e] += in ? rb : bb[e];
-                    a[e] = ra;
-                    bb[e] = rb;
+                    const bool in0 = (each >> e) & 1u, in1 = (each >> (e + 1)) & 1u;
+                    const float2 t0 =
+                        ptx::add2({acc0[e], acc0[e + 1]}, {in0 ? ra.x : a2.x, in1 ? ra.y : a2.y});
+                    const float2 t1 =
+                        ptx::add2({acc1[e], acc1[e + 1]}, {in0 ? rb.x : b2.x, in1 ? rb.y : b2.y});
+                    acc0[e] = t0.x;
+                    acc0[e + 1] = t0.y;
+                    acc1[e] = t1.x;
+                    acc1[e + 1] = t1.y;
+                    a[e] = ra.x;
+                    a[e + 1] = ra.y;
+                    bb[e] = rb.x;
+                    bb[e + 1] = rb.y;
                 }
                 if (k_rot != nullptr) {
                     T* orow = k_rot + (bh * (int64_t)p.L + c0 + r) * D + u * V;
@@ -317,44 +338,59 @@ __global__ void __launch_bounds__(256) summaries_axes_kernel(
                 acc1[e] += __shfl_xor_sync(0xffffffffu, acc1[e], off);
             }
         }
-        auto finish = [&](const float* s0, const float* s1, int i, int n, S* out) {
-            float o0[V], o1[V];
-            const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float m0 = s0[e] * inv_n, m1 = s1[e] * inv_n;
-                const float c = s_mc[i][u * V + e], sn = s_ms[i][u * V + e];
-                const bool on = n > 0 && ((mean >> e) & 1u);
-                o0[e] = on ? m0 * c - m1 * sn : m0;
-                o1[e] = on ? m0 * sn + m1 * c : m1;
-            }
-            store_sum(out + u * V, o0, V);
-            store_sum(out + half + u * V, o1, V);
-        };
         if (q == 0) {
-            finish(acc0, acc1, g, n_g, gs + ((bh * p.nC + ch) * G + g) * (int64_t)D);
+            float* sums = s_sum + ((h - h0) * G + g) * D + u * V;
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
-                *reinterpret_cast<float4*>(&s_sum[h & 1][g][u * V + e]) =
-                    *reinterpret_cast<const float4*>(acc0 + e);
-                *reinterpret_cast<float4*>(&s_sum[h & 1][g][half + u * V + e]) =
-                    *reinterpret_cast<const float4*>(acc1 + e);
+                *reinterpret_cast<float4*>(sums + e) = *reinterpret_cast<const float4*>(acc0 + e);
+                *reinterpret_cast<float4*>(sums + half + e) = *reinterpret_cast<const float4*>(acc1 + e);
             }
         }
-        __syncthreads();
-        if (tid < L) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                acc0[e] = acc1[e] = 0.f;
-                for (int y = 0; y < G; ++y) {
-                    acc0[e] += s_sum[h & 1][y][u * V + e];
-                    acc1[e] += s_sum[h & 1][y][half + u * V + e];
-                }
-            }
-            finish(acc0, acc1, 8, n_rows, cs + (bh * p.nC + ch) * (int64_t)D);
-        }
-        // the other parity's sums are free: their readers came through this barrier
     }
+    __syncthreads();
+    // the means of every head's groups and chunk (sum i = G), turned by the mean
+    // angle where the pair is low: V pairs a thread
+    for (int x = tid; x < (h1 - h0) * (G + 1) * L; x += 32 * G) {
+        const int slice = x % L, i = x / L % (G + 1), h = x / L / (G + 1);
+        const float* sums = s_sum + (h * G + (i < G ? i : 0)) * D + slice * V;
+        float a[V], bb[V];
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            *reinterpret_cast<float4*>(a + e) = *reinterpret_cast<const float4*>(sums + e);
+            *reinterpret_cast<float4*>(bb + e) = *reinterpret_cast<const float4*>(sums + half + e);
+        }
+        if (i == G) {
+            for (int y = 1; y < G; ++y)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    a[e] += sums[y * D + e];
+                    bb[e] += sums[y * D + half + e];
+                }
+        }
+        const int n = i == G ? n_rows : min(max(n_rows - kGroupRows * i, 0), kGroupRows);
+        const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int pair = slice * V + e;
+            a[e] *= inv_n;
+            bb[e] *= inv_n;
+            const float c = s_mc[i * half + pair], sn = s_ms[i * half + pair];
+            if (c != kNoTurn && n > 0) {
+                const float m0 = a[e], m1 = bb[e];
+                a[e] = m0 * c - m1 * sn;
+                bb[e] = m0 * sn + m1 * c;
+            }
+        }
+        const int64_t bh = b * p.Hkv + h0 + h, chunk = bh * p.nC + ch;
+        S* out = (i == G ? cs + chunk * D : gs + (chunk * G + i) * D) + slice * V;
+        store_sum(out, a, V);
+        store_sum(out + half, bb, V);
+    }
+}
+
+// Bytes of the kernel's dynamic shared memory (at most 102 KB).
+size_t summaries_smem(const Params& p, int hp) {
+    return ((size_t)p.C * p.d + (size_t)(p.G + 1) * p.d + (size_t)hp * p.G * p.d) * sizeof(float);
 }
 
 }  // namespace
@@ -408,8 +444,9 @@ cudaError_t launch_summaries_axes(const Params& p, const AxisMap& am, const int3
                                   const void* k_raw, void* chunk_sum, void* group_sum,
                                   void* k_rot, int chunk_begin, int chunk_end, cudaStream_t st) {
     using bf = __nv_bfloat16;
-    // heads per CTA: all of them, halved while the grid is short of four CTAs per SM
-    int hp = p.Hkv;
+    // heads per CTA: all of them up to 8, halved while the grid is short of four
+    // CTAs per SM
+    int hp = p.Hkv < 8 ? p.Hkv : 8;
     auto ctas = [&](int n) {
         return (int64_t)(chunk_end - chunk_begin) * p.B * ((p.Hkv + n - 1) / n);
     };
@@ -417,13 +454,13 @@ cudaError_t launch_summaries_axes(const Params& p, const AxisMap& am, const int3
     const int groups = (p.Hkv + hp - 1) / hp;
     if (p.B > 65535 || groups > 65535) return cudaErrorInvalidValue;
     const dim3 grid(chunk_end - chunk_begin, p.B, groups);
-    const size_t smem = (size_t)p.C * p.d * sizeof(float);
+    const size_t smem = summaries_smem(p, hp);
     auto run = [&](auto t, auto s, auto d) {
         using T = decltype(t);
         using S = decltype(s);
         auto* kernel = summaries_axes_kernel<T, S, decltype(d)::value>;
         const cudaError_t e = set_func_attr_once(
-            (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 128 * 4);
+            (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 104 * 1024);
         if (e != cudaSuccess) return e;
         kernel<<<grid, 32 * p.G, smem, st>>>(p, am, positions, (const T*)k_raw, (S*)chunk_sum,
                                             (S*)group_sum, (T*)k_rot, chunk_begin, hp);
