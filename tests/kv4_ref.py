@@ -94,7 +94,12 @@ def attend(cfg, q, k, v, sel, n_sel):
     (a sum of D products in fp32) plus 2^-20 for the exponential, so numerator
     and denominator are each off by at most r = 2^-8 + ds + 2^-20 relative to
     sum w |v| and sum w; with the sums over n keys in fp32 (n 2^-24) and the
-    output's own rounding."""
+    output's own rounding. Besides, fp16 has no step below 2^-24: a weight below 2^-14
+    is off by up to 2^-25 absolutely. Weights are relative to a maximum that was a score
+    of the row when it was taken, so that score's own weight is 1 and sum w >= 1; n
+    weights so rounded move the numerator by n 2^-25 max|v| and the denominator by
+    n 2^-25, the output by n 2^-25 (max|v| + |o|) (weights rounded against an earlier,
+    smaller maximum shrink with it)."""
     B, T, Hq, _ = q.shape
     Hu = sel.shape[1]
     out = torch.zeros(B, T, Hq, D, dtype=torch.float64)
@@ -112,7 +117,8 @@ def attend(cfg, q, k, v, sel, n_sel):
                 ds = (D + 8) * F32 * float((kk.abs() @ x.abs()).max()) / math.sqrt(D)
                 out[b, t, h] = w @ vv
                 r = BF16 + ds + 2.0 ** -20 + len(at) * F32
-                tol[b, t, h] = 2 * r * (w @ vv.abs()) + BF16 * out[b, t, h].abs() * (1 + 2 * r) + 1e-30
+                tol[b, t, h] = 2 * r * (w @ vv.abs()) + BF16 * out[b, t, h].abs() * (1 + 2 * r) + (
+                    len(at) * 2.0 ** -25 * (vv.abs().amax(0) + out[b, t, h].abs()) * (1 + 2 * r))
     return out, tol
 
 

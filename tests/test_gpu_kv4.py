@@ -189,6 +189,30 @@ def test_attend_decode_large_queries():
     _check(out, want, tol)
 
 
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("q_begin,q_len", [(639, 1), (512, 128), (560, 33)])
+def test_attend_scores_that_rise(order, q_begin, q_len):
+    """Keys whose scores grow by orders of magnitude from block to block (the running
+    maximum is raised again and again), or shrink, for some heads only."""
+    from long_context_rope_b200 import hga
+    cfg = _cfg4(hga, seq_len=640, q_begin=q_begin, q_len=q_len, n_sink=1, n_local=1, top_k_groups=24,
+                k_scale=2.0 ** -4)
+    k = _rows((1, 1, 640, 128), 130).float()
+    size = torch.arange(640) / 16
+    size = {"rising": size, "falling": 40 - size, "mixed": (size * 7) % 40}[order].floor()
+    k *= (1 + size)[:, None] ** 1.5
+    q = _rows((1, q_len, 8, 128), 131)
+    q[:, :, :3] *= 0.01
+    kp = R.pack(*R.quantise(k.to(BF), cfg.k_scale))
+    vp = R.pack(*R.quantise(_rows((1, 1, 640, 128), 132), cfg.v_scale))
+    sel, n = R.lists(cfg, 1, 133)
+    want, tol = R.attend(cfg, q, R.values(kp, cfg.k_scale), R.values(vp, cfg.v_scale), sel, n)
+    out = torch.empty_like(q).cuda()
+    hga.attend(cfg, q.cuda(), kp.cuda(), vp.cuda(), sel.cuda(), n.cuda(), out)
+    _clean(hga)
+    _check(out, want, tol)
+
+
 PREFILL = [
     dict(seq_len=2, q_len=2), dict(seq_len=65, q_len=65), dict(seq_len=300, q_len=300),
     dict(seq_len=700, q_begin=333, q_len=250), dict(seq_len=640, q_begin=128, q_len=512, batch=2,
