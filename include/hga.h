@@ -104,7 +104,7 @@ typedef enum { HGA_KV_FULL = 0, HGA_KV_WINDOWS = 1 } hga_kv_layout;
  *                   values). Written by hga_build_summaries; read by
  *                   hga_route and hga_decode_step on their one-launch decode
  *                   path (one query token, bf16, d = 128, gq <= 8, L % 16 ==
- *                   0, top_k_chunks <= 64); every other routing call returns
+ *                   0 or HGA_KV_E2M1, top_k_chunks <= 64); every other routing call returns
  *                   HGA_ERR_UNSUPPORTED for it. */
 typedef enum { HGA_SUMMARY_F32 = 0, HGA_SUMMARY_BF16 = 1 } hga_summary_type;
 
@@ -187,8 +187,8 @@ typedef struct {
     int32_t kv_layout;         /* hga_kv_layout, read by hga_attend only */
     int32_t summary_type;      /* hga_summary_type of the summary tables (0 = fp32) */
     int32_t kv_type;           /* hga_kv_type of keys and values (0 = cfg->dtype) */
-    float k_scale;             /* HGA_KV_E4M3: scale of the key codes (finite, > 0) */
-    float v_scale;             /* HGA_KV_E4M3: scale of the value codes (finite, > 0) */
+    float k_scale;             /* HGA_KV_E4M3, HGA_KV_E2M1: scale of the key codes (finite, > 0) */
+    float v_scale;             /* HGA_KV_E4M3, HGA_KV_E2M1: of the value codes (finite, > 0) */
     int32_t routing;           /* hga_routing (0 = per KV head) */
 } hga_config;
 
@@ -325,10 +325,10 @@ hga_status hga_route(const hga_config* cfg, const void* q_rot, const void* chunk
  * [B, Hkv, L, d] (cfg->kv_layout must be HGA_KV_FULL; the host tier goes
  * through hga_route, hga_gather_kv and hga_attend). Writes q-bar, both
  * selections (as hga_route) and out [B, q_len, Hq, d]. For a one-token query
- * span (decode) in bf16, d = 128, gq <= 8, L % 16 == 0, top_k_chunks <= 64
- * this is a single launch: the always-visible blocks are fetched while the
- * routing runs; the attention result equals hga_attend's within fp32
- * summation order. Other configurations run the separate kernels. */
+ * span (decode) in bf16, d = 128, gq <= 8, L % 16 == 0 (any L with
+ * HGA_KV_E2M1), top_k_chunks <= 64 this is a single launch: the
+ * always-visible blocks are fetched while the routing runs; the attention
+ * result equals hga_attend's within fp32 summation order. Other configurations run the separate kernels. */
 hga_status hga_decode_step(const hga_config* cfg, const void* q_rot, const void* chunk_sum,
                            const void* group_sum, const void* k_cache, const void* v_cache,
                            float* qbar_out, int32_t* sel_chunks, int32_t* n_sel_chunks,

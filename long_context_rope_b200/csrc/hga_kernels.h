@@ -103,7 +103,8 @@ cudaError_t launch_attend_simt(const Params& p, const void* q_rot, const KvSourc
 
 // True when a tcgen05 prefill kernel covers this configuration (d = 128,
 // prefill, full resident store, index mode; bf16 with 8 query heads per KV
-// head, or the 4-bit store with up to 128).
+// head, or the 4-bit store with up to 128, single tokens of more than 8 heads
+// among them).
 bool tc_kernel_supports(const Params& p, bool gathered);
 
 cudaError_t launch_attend_tc(const Params& p, const void* q_rot, const KvSources& kv,

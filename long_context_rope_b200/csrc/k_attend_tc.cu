@@ -484,9 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 }  // namespace
 
 bool tc_kernel_supports(const Params& p, bool gathered) {
-    if (p.q_len <= 1 || gathered || p.kv_layout != HGA_KV_FULL) return false;
-    if (p.kv_f4) return p.gq <= kRows;
-    return p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.C % 32 == 0;
+    if (gathered || p.kv_layout != HGA_KV_FULL) return false;
+    // a decode step of more than 8 heads, which the decode kernels do not take, too
+    if (p.kv_f4) return p.gq <= kRows && (p.q_len > 1 || p.gq > 8);
+    return p.q_len > 1 && p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.C % 32 == 0;
 }
 
 cudaError_t launch_attend_tc(const Params& p, const void* q_rot, const KvSources& kv,
