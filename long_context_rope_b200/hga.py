@@ -245,7 +245,7 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=Tr
     # its host time); what is wrong with another one, below
     if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype)
             and (shape is None or t.shape == shape) and t.is_contiguous()
-            and (not device or t.get_device() == torch._C._cuda_getDevice())):
+            and (not device or t.is_cuda and t.get_device() == torch._C._cuda_getDevice())):
         return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is required")

@@ -95,10 +95,20 @@ def alloc_store(cfg: hga.HgaConfig, device="cuda"):
             torch.zeros(shape, dtype=cfg.kv_torch_dtype(), device=device))
 
 
+def _check_axes(axes, positions, shape) -> None:
+    """Axes come with positions of `shape` (their leading n_axes left out), and positions with axes."""
+    if (axes is None) != (positions is None):
+        raise ValueError("axes and positions go together")
+    if axes is not None and tuple(positions.shape) != (axes.n_axes, *shape):
+        raise ValueError(f"positions must have shape {(axes.n_axes, *shape)}, "
+                         f"got {tuple(positions.shape)}")
+
+
 def rotate_queries(cfg: hga.HgaConfig, q_raw: torch.Tensor, stream=None, axes=None,
                    positions=None) -> torch.Tensor:
     """Rotate queries [B, q_len, Hq, d] by their token positions, or with axes by
     positions [n_axes, B, q_len] int32."""
+    _check_axes(axes, positions, (cfg.batch, cfg.q_len))
     q_rot = torch.empty_like(q_raw)
     if axes is not None:
         hga.apply_rope_axes(cfg, axes, positions, q_raw, q_rot, cfg.batch, cfg.q_len, cfg.n_q_heads,
@@ -112,6 +122,7 @@ def summaries(cfg: hga.HgaConfig, k_raw, cs, gs, k_rot=None, stream=None, axes=N
               positions=None, chunk_begin: int = 0, chunk_end: Optional[int] = None):
     """Key summaries (and rotated keys) of chunks [chunk_begin, chunk_end), by token
     position or with axes by positions [n_axes, B, L] int32."""
+    _check_axes(axes, positions, (cfg.batch, cfg.seq_len))
     chunk_end = cfg.n_chunks if chunk_end is None else chunk_end
     if axes is not None:
         hga.build_summaries_axes(cfg, axes, positions, k_raw, cs, gs, k_rot, chunk_begin, chunk_end,
@@ -236,6 +247,7 @@ def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new,
     v_cache are 4-bit stores and the token goes into both in one launch
     (hga_store_kv)."""
     B, H, d = cfg_cap.batch, cfg_cap.n_kv_heads, cfg_cap.head_dim
+    _check_axes(axes, positions, (B, cfg_cap.seq_len))
     k_new_raw = k_new_raw.contiguous()
     at = None if positions is None else positions[:, :, pos:pos + 1].contiguous()
     k_raw_cache[:, :, pos].copy_(k_new_raw, non_blocking=True)

@@ -145,3 +145,39 @@ def test_binding_refusals(hga):
             hga.load_kv(cfg, st, st, bad, k, 0)
     with pytest.raises(ValueError):
         hga.store_kv(cfg, k, k, st, st, 0, positions=torch.zeros(1, 1, 2, dtype=torch.int32))
+
+
+def test_tensor_of_the_cpu_is_a_value_error(hga):
+    """With or without a driver, a right tensor in the wrong place is refused by name."""
+    import torch
+    cfg = _cfg(hga)
+    x = torch.zeros(1, 4, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        hga.apply_rope(cfg, x, x, 1, 4, 1, 0)
+    pos = torch.zeros(1, 1, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        hga.apply_rope_axes(cfg, hga.rope_axes([0], 1), pos, x, x, 1, 4, 1)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_axes_and_positions_go_together(hga, kv4):
+    """Refused before anything is launched or written: positions without axes (they would
+    be passed over), axes without positions, positions of another shape."""
+    import torch
+    from long_context_rope_b200 import pipeline
+    cfg = (_cfg4 if kv4 else _cfg)(hga, batch=1, seq_len=64, q_begin=0, q_len=64)
+    ax = hga.rope_axes([0, 1] * 32, 2)
+    right = torch.zeros(2, 1, 64, dtype=torch.int32)
+    k = torch.zeros(1, cfg.n_kv_heads, 64, 128, dtype=torch.bfloat16)
+    q = torch.zeros(1, 64, cfg.n_q_heads, 128, dtype=torch.bfloat16)
+    cs, gs, rb, out = None, None, None, None
+    for axes, pos in ((None, right), (ax, None), (ax, right[:, :, :63]), (ax, right[:1])):
+        with pytest.raises(ValueError, match="positions"):
+            pipeline.rotate_queries(cfg, q, axes=axes, positions=pos)
+        with pytest.raises(ValueError, match="positions"):
+            pipeline.summaries(cfg, k, cs, gs, axes=axes, positions=pos)
+        with pytest.raises(ValueError, match="positions"):
+            pipeline.prefill(cfg, k, k, q, cs, gs, None, rb, out, axes=axes, positions=pos)
+        with pytest.raises(ValueError, match="positions"):
+            pipeline.decode_append(cfg, 3, k[:, :, 0], k[:, :, 0], q[:, :1], k, None, None, cs, gs,
+                                   rb, out, axes=axes, positions=pos)
