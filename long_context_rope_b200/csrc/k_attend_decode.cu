@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
     DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(
         align_smem_1024(smem_raw));
     cg::cluster_group cluster = cg::this_cluster();
+    ptx::cluster_started_arrive();
     const int CL = (int)cluster.num_blocks();
     const int r = (int)cluster.block_rank();
     const int64_t bh = blockIdx.y;  // routing unit: (sequence, KV head) or (sequence, query head)
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_decode_kernel(
     // ---- per-warp partials -> shared memory (the ring's space is reused)
     if (warp < kConsumers) dec::store_warp_partial<kF8>(acc, sm.u.warp_part[warp]);
     __syncthreads();
+    ptx::cluster_started_wait();
     dec::merge_warps_push(sm.u.warp_part, cluster, sm.owned, sm.wgt, p.gq);
     cluster.sync();  // every partial is in its owner's shared memory
     dec::merge_owned_and_store(p, (int)cluster.num_blocks(), (int)cluster.block_rank(), sm.owned, b,

@@ -12,9 +12,9 @@
 // routed list) goes to warp i mod 4 CL of the cluster, and each warp works out
 // its own blocks from the list, so a CTA starts without a barrier. (CTAs of
 // eight warps, two per SM: the same up to 296 units, where all are resident
-// either way; 43 against 41 us for 512 units of 108 pages, which then take two
-// rounds of CTAs.) Bound by instructions, about 390 a page, at 16 warps an SM:
-// 127 MB in 41 us.
+// either way; two us more for 512 units of 108 pages, which then take two rounds of
+// CTAs.) Bound by instructions, about 390 a page, at 16 warps an SM: 127 MB in
+// 37 us.
 // hga_decode_pages.cuh has the arithmetic and the joining of the partials.
 #include <cooperative_groups.h>
 
@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) attend_pages_kernel(
     extern __shared__ __align__(128) uint8_t smem_raw[];
     PagesSmem& sm = *reinterpret_cast<PagesSmem*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
+    ptx::cluster_started_arrive();
     const int CL = (int)cluster.num_blocks(), r = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t bh = blockIdx.y;  // routing unit: (sequence, KV head) or (sequence, query head)
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) attend_pages_kernel(
             return dec::page_at((page & kSrcGathered) ? gbase : rbase, page & ~kSrcGathered);
         },
         [&](int i) { return sm.blk[warp][i].y; }, acc);
+    ptx::cluster_started_wait();
     dec::merge_pages<kWarps>(sm, cluster, p, acc, b, h, out);
 }
 

@@ -11,10 +11,11 @@
 // copied: four warps widen the codes of a page row to 16 bits, times their
 // block scales, straight into the swizzled operand tiles. Code x block scale
 // has at most 6 significant bits, so that is exact in either type. Keys become
-// bf16, the queries' type (three more instructions per pair of elements than
+// bf16, the queries' type: three more instructions per pair of elements than
 // fp16, but queries in fp16 would have to be scaled row by row to keep bf16's
-// range, which held up every unit's start: 571 us for the last 16K tokens of
-// 32K). Values become fp16, and so does P (at most 2^8, by the lazy rescaling).
+// range (571 against 577 us at the time, and a longer start of every unit, which
+// copies that go past the registers shorten). Values become fp16, and so does P
+// (at most kMaxSum).
 //
 // Sixteen warps in four warpgroups, which split the registers:
 //   warps 0..3, 4..7  softmax of M tile A, B (152 registers a thread);
@@ -24,6 +25,13 @@
 //   warps 12..15      tiles (104): thread r owns key row r of every K and V
 //                     tile, whose next codes it holds in registers while it
 //                     widens the current ones.
+//
+// Bound by the alternation of products and softmax within a unit (the tensor
+// cores wait while a tile's weights are made; both M tiles in turn hide most of
+// it) and by the start and end of units, 8000 cycles each: 32 heads over 4, the
+// last 16K tokens of 32K in 508 to 521 us (908 to 931 TFLOP/s), 4K tokens in 113
+// to 119 us.
+//
 // An M tile holds 128 / gq whole tokens (all gq heads of each), so any number
 // of query heads per KV head up to 128 is served; rows past that are idle.
 //

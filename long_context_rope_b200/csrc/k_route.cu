@@ -17,6 +17,7 @@
 
 
 #include "hga_kernels.h"
+#include "hga_ptx.cuh"
 #include "hga_topk.cuh"
 
 namespace cg = cooperative_groups;
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(256) route_chunks_kernel(Params p, float* __re
                                                            float* __restrict__ scores) {
     extern __shared__ uint32_t keys[];     // [nC] candidate keys, then 256 histogram words
     cg::cluster_group cluster = cg::this_cluster();
+    ptx::cluster_started_arrive();
     const int CL = (int)cluster.num_blocks();
     const int r = (int)cluster.block_rank();
     const int jj = blockIdx.y;
@@ -171,6 +173,7 @@ __global__ void __launch_bounds__(256) route_chunks_kernel(Params p, float* __re
     const int c_lo = r * per;
     const int c_hi = c_lo + per < j ? c_lo + per : j;
     const float* table = cs + bh * (int64_t)p.nC * p.d;
+    ptx::cluster_started_wait();
     for (int c0 = c_lo + warp * kRowsInFlight; c0 < c_hi; c0 += nw * kRowsInFlight) {
         float v[kRowsInFlight][DPL];
 #pragma unroll
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(256) route_groups_kernel(
     extern __shared__ uint32_t keys[];     // [kc*G] candidate keys, then 256 histogram words
     __shared__ int s_chunk[1024];  // validated chunk of each slot, -1 if invalid
     cg::cluster_group cluster = cg::this_cluster();
+    ptx::cluster_started_arrive();
     const int CL = (int)cluster.num_blocks();
     const int r = (int)cluster.block_rank();
     const int jj = blockIdx.y;
@@ -253,6 +257,7 @@ __global__ void __launch_bounds__(256) route_groups_kernel(
     const int x_lo = r * per;
     const int x_hi = x_lo + per < ncand ? x_lo + per : ncand;
     const float* table = gs + bh * (int64_t)p.nC * p.G * p.d;
+    ptx::cluster_started_wait();
     for (int x0 = x_lo + warp * kRowsInFlight; x0 < x_hi; x0 += nw * kRowsInFlight) {
         float v[kRowsInFlight][DPL];
 #pragma unroll
