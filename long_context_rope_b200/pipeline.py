@@ -227,6 +227,11 @@ def fill_windows(cfg: hga.HgaConfig, k_full, v_full, k_win, v_win):
         v_win[:, :, w * C: w * C + hi - c * C].copy_(v_full[:, :, c * C: hi], non_blocking=True)
 
 
+def _as_stream(stream) -> torch.cuda.Stream:
+    """A stream given as torch's object or as its handle."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
 def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new, k_raw_cache,
                   k_rot_cache, v_cache, cs, gs, rb: RouteBuffers, out, stream=None, axes=None,
                   positions=None):
@@ -245,7 +250,12 @@ def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new,
     With axes, the key turns by positions[:, :, pos] of positions
     [n_axes, B, capacity] int32 instead. With kv_type E2M1, k_rot_cache and
     v_cache are 4-bit stores and the token goes into both in one launch
-    (hga_store_kv)."""
+    (hga_store_kv). All of the step runs on `stream` (torch's current one by
+    default)."""
+    if stream is not None:  # the copies between the launches belong on it too
+        with torch.cuda.stream(_as_stream(stream)):
+            return decode_append(cfg_cap, pos, k_new_raw, v_new, q_rot_new, k_raw_cache,
+                                 k_rot_cache, v_cache, cs, gs, rb, out, None, axes, positions)
     B, H, d = cfg_cap.batch, cfg_cap.n_kv_heads, cfg_cap.head_dim
     _check_axes(axes, positions, (B, cfg_cap.seq_len))
     k_new_raw = k_new_raw.contiguous()

@@ -776,3 +776,44 @@ def test_other_device_is_refused():
     for bad in (k, k.cuda().transpose(2, 3).contiguous().transpose(2, 3), k.cuda().float()):
         with pytest.raises(ValueError):
             hga.store_kv(cfg, bad, k.cuda(), st, st, 0)
+
+
+@pytest.mark.parametrize("kv4,handle", [(False, False), (True, False), (True, True)])
+def test_append_on_another_stream(kv4, handle):
+    """A decode step given a stream runs on it whole: its copies do not wait for what the
+    current stream is busy with, so the step sees its own token there."""
+    from long_context_rope_b200 import hga, pipeline
+    L0, kw = 70, dict(batch=1, n_kv_heads=2, n_q_heads=16, seq_len=128)
+    cfg = _cfg4(hga, **kw) if kv4 else _cfg4(hga, kv_type=hga.HGA_KV_AS_DTYPE, **kw)
+    k, v = _rows((1, 2, 128, 128), 90).cuda(), _rows((1, 2, 128, 128), 91).cuda()
+    axes = hga.rope_axes([0, 1] * 32, 2)
+    pos = torch.randint(0, 99, (2, 1, 128), dtype=torch.int32,
+                        generator=torch.Generator().manual_seed(92)).cuda()
+    q = _rows((1, 1, 16, 128), 93).cuda()
+    outs = []
+    side = torch.cuda.Stream()
+    for other in (False, True):
+        kc = torch.zeros_like(k)
+        kr, vs = pipeline.alloc_store(cfg)
+        cs, gs = pipeline.alloc_summaries(cfg)
+        cs.zero_(), gs.zero_()
+        rb = pipeline.alloc_route(cfg.copy(q_begin=0, q_len=1))
+        out = torch.full_like(q, float("nan"))
+        torch.cuda.synchronize()
+        if other:
+            torch.cuda._sleep(400_000_000)  # some 0.2 s of the current stream
+        st = None if not other else (side.cuda_stream if handle else side)
+        for t in range(60, L0):             # a chunk's end among them
+            pipeline.decode_append(cfg, t, k[:, :, t], v[:, :, t], q, kc, kr, vs, cs, gs, rb, out,
+                                   stream=st, axes=axes, positions=pos)
+        side.synchronize()
+        got = [x.to("cpu") for x in (out, kc, kr, vs, cs[:, :, :1], gs[:, :, :4])] if not other else None
+        if other:
+            with torch.cuda.stream(side):
+                got = [x.clone() for x in (out, kc, kr, vs, cs[:, :, :1], gs[:, :, :4])]
+            torch.cuda.synchronize()
+            got = [x.cpu() for x in got]
+        _clean(hga)
+        outs.append(got)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
