@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_axes_kernel(
 // wait in shared memory for the end, where all threads turn them into means (a
 // barrier and a tail per head took two thirds of a head's time). The chunk's sums
 // go over the groups in order. Mean positions are sums of integers, exact to
-// double rounding. 64K tokens x 4 heads (145 MB with the rotated keys) in 47 us,
-// 3.1 TB/s: the angles of a chunk and the rotation's instructions, with one
-// head's rows in flight, bound it, not the memory.
+// double rounding. A token's rows of the next head are loaded as soon as the
+// current ones are unpacked. 64K tokens x 4 heads (145 MB with the rotated keys)
+// in 43 us, 3.4 TB/s: the angles of a chunk and the rotation's instructions bound
+// it, not the memory (5 or 6 CTAs an SM, at 96 or 80 registers: 47.5, 60 us).
 //
 // In the tables, 16-byte piece j of a row sits at j ^ (j >> 3), so that the
 // eight lanes of a row read different banks.
@@ -209,17 +210,14 @@ __global__ void __launch_bounds__(256, 2) summaries_axes_kernel(
     float* s_sum = s_ms + (G + 1) * half;
 
     typename Vec<T>::Raw raw_a[R], raw_b[R];
-    auto load_rows = [&](int h) {
-        const T* base = k_raw + ((b * p.Hkv + h) * (int64_t)p.L + c0 + row0) * D + u * V;
-#pragma unroll
-        for (int m = 0; m < R; ++m) {
-            if (row0 + m < n_rows) {
-                raw_a[m] = Vec<T>::load_raw(base + m * D);
-                raw_b[m] = Vec<T>::load_raw(base + m * D + half);
-            }
-        }
+    const T* k_rows = k_raw + ((b * p.Hkv + h0) * (int64_t)p.L + c0 + row0) * D + u * V;
+    auto load_row = [&](int m) {
+        raw_a[m] = Vec<T>::load_raw(k_rows + m * D);
+        raw_b[m] = Vec<T>::load_raw(k_rows + m * D + half);
     };
-    load_rows(h0);
+#pragma unroll
+    for (int m = 0; m < R; ++m)
+        if (row0 + m < n_rows) load_row(m);
     const int left = n_rows - kGroupRows * g;  // tokens of this group, if positive
     const int n_g = left <= 0 ? 0 : (left >= kGroupRows ? kGroupRows : left);
     for (int a = 0; a < am.n_axes; ++a) {
@@ -278,22 +276,30 @@ __global__ void __launch_bounds__(256, 2) summaries_axes_kernel(
         turn |= (on && (!low || k_rot != nullptr) ? 1u : 0u) << e;
         each |= (on && !low ? 1u : 0u) << e;
     }
-    // the whole warp's pairs are rotated token by token (the rotated keys are wanted)
-    const bool all = __all_sync(0xffffffffu, turn == (1u << V) - 1u) != 0;
+    // the whole warp's pairs are rotated (the rotated keys are wanted), and each
+    // lane's are all or none token by token in the sums: no select per pair
+    constexpr unsigned kFull = (1u << V) - 1u;
+    const bool plain =
+        __all_sync(0xffffffffu, turn == kFull && (each == 0u || each == kFull)) != 0;
     __syncthreads();
 
     for (int h = h0; h < h1; ++h) {
         const int64_t bh = b * p.Hkv + h;
+        k_rows += (int64_t)p.L * D;  // the next head's
         float acc0[V], acc1[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc0[e] = acc1[e] = 0.f;
+        auto rows = [&](auto is_plain) {
+            constexpr bool kPlain = decltype(is_plain)::value;
+            const bool lane_in = each != 0u;
 #pragma unroll
-        for (int m = 0; m < R; ++m) {
-            const int r = row0 + m;
-            if (r < n_rows) {
+            for (int m = 0; m < R; ++m) {
+                const int r = row0 + m;
+                if (r >= n_rows) break;
                 float a[V], bb[V], c[V], sn[V];
                 Vec<T>::unpack(raw_a[m], a);
                 Vec<T>::unpack(raw_b[m], bb);
+                if (h + 1 < h1) load_row(m);
 #pragma unroll
                 for (int e = 0; e < V; e += 4) {
                     const int at = table_at(r, u * V + e, half);
@@ -307,12 +313,13 @@ __global__ void __launch_bounds__(256, 2) summaries_axes_kernel(
                     const float2 c2 = {c[e], c[e + 1]}, s2 = {sn[e], sn[e + 1]};
                     float2 ra = ptx::sub2(ptx::mul2(a2, c2), ptx::mul2(b2, s2));
                     float2 rb = ptx::fma2(a2, s2, ptx::mul2(b2, c2));
-                    if (!all) {
+                    if (!kPlain) {
                         const bool on0 = (turn >> e) & 1u, on1 = (turn >> (e + 1)) & 1u;
                         ra = {on0 ? ra.x : a2.x, on1 ? ra.y : a2.y};
                         rb = {on0 ? rb.x : b2.x, on1 ? rb.y : b2.y};
                     }
-                    const bool in0 = (each >> e) & 1u, in1 = (each >> (e + 1)) & 1u;
+                    const bool in0 = kPlain ? lane_in : (each >> e) & 1u;
+                    const bool in1 = kPlain ? lane_in : (each >> (e + 1)) & 1u;
                     const float2 t0 =
                         ptx::add2({acc0[e], acc0[e + 1]}, {in0 ? ra.x : a2.x, in1 ? ra.y : a2.y});
                     const float2 t1 =
@@ -332,8 +339,11 @@ __global__ void __launch_bounds__(256, 2) summaries_axes_kernel(
                     Vec<T>::store(orow + half, bb);
                 }
             }
-        }
-        if (h + 1 < h1) load_rows(h + 1);  // in flight over the reductions
+        };
+        if (plain)
+            rows(std::true_type());
+        else
+            rows(std::false_type());
 #pragma unroll
         for (int e = 0; e < V; ++e) {
 #pragma unroll
@@ -450,7 +460,7 @@ cudaError_t launch_summaries_axes(const Params& p, const AxisMap& am, const int3
     using bf = __nv_bfloat16;
     // heads per CTA: all of them up to 8, halved while the grid is short of two
     // CTAs per SM: fewer heads share a chunk's angles less (237 chunks of 8 heads:
-    // 28.7 us in 474 CTAs, 36.9 in 948, 32.8 in 237)
+    // 24.8 us in 474 CTAs, 31.5 in 948)
     int hp = p.Hkv < 8 ? p.Hkv : 8;
     auto ctas = [&](int n) {
         return (int64_t)(chunk_end - chunk_begin) * p.B * ((p.Hkv + n - 1) / n);
