@@ -1,17 +1,20 @@
-"""Build libhga.so (sm_100a) in-tree with nvcc.
+"""Build libhga.so (sm_100a) in-tree with nvcc, and its Python binding with g++.
 
 Each CUDA source under csrc/ is compiled to an object in _build/ (in
-parallel), then linked into long_context_rope_b200/libhga.so. Run as
+parallel), then linked into long_context_rope_b200/libhga.so; csrc/py_bind.cpp
+becomes long_context_rope_b200/_hga_bind.so, which links to it. Run as
 ``python -m long_context_rope_b200.build`` or call ``build()``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhga.so")
+BIND = os.path.join(PKG, "_hga_bind.so")
+BIND_SRC = os.path.join(CSRC, "py_bind.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -49,7 +54,8 @@ def _stale(target: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
-    """Compile every CUDA source for sm_100a and link libhga.so. Returns its path."""
+    """Compile every CUDA source for sm_100a, link libhga.so and build its Python
+    binding. Returns the library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
     srcs, hdrs = _sources(), _headers()
     objs = []
@@ -78,7 +84,25 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link of libhga.so failed")
         os.replace(tmp, LIB)
+    if force or _stale(BIND, [BIND_SRC, os.path.join(INCLUDE, "hga.h")]):
+        _build_bind()
     return LIB
+
+
+def _build_bind() -> None:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BIND + f".tmp{os.getpid()}"
+    inc = os.path.join(torch_dir, "include")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
+           "-isystem" + os.path.join(inc, "torch", "csrc", "api", "include"), BIND_SRC, "-o", tmp,
+           f"-L{PKG}", "-l:libhga.so", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        raise RuntimeError("build of _hga_bind.so failed")
+    os.replace(tmp, BIND)
 
 
 if __name__ == "__main__":

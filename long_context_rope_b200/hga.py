@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libhga.so (the C ABI declared in include/hga.h).
+"""Thin binding of libhga.so (the C ABI declared in include/hga.h): the hot path's
+calls and their tensor checks through _hga_bind.so, the rest through ctypes.
 
 Argument marshalling only: each function checks that the torch tensors it is
 given live on the current CUDA device with the dtype, shape and contiguity
@@ -6,7 +7,7 @@ the call expects, passes their data pointers and the current CUDA stream to
 the C entry point of the same name, and raises HgaError on a non-OK status.
 Every step of the hot path runs in the library's kernels; there is no other
 implementation behind these functions. Importing this module fails loudly if
-libhga.so has not been built.
+libhga.so or _hga_bind.so has not been built.
 """
 from __future__ import annotations
 
@@ -201,6 +202,12 @@ def _load():
 
 _lib = _load()
 
+try:
+    from . import _hga_bind as _bind
+except ImportError as e:
+    raise ImportError(f"_hga_bind.so cannot be loaded ({e}): build the library first "
+                      "(python -m long_context_rope_b200.build)") from e
+
 
 def library() -> ctypes.CDLL:
     return _lib
@@ -236,18 +243,12 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=True,
-         nullable=False) -> Optional[int]:
-    """Address of a tensor that has the type, shape, place and layout asked for."""
-    if t is None and nullable:
-        return None
-    # one pass for a tensor that is as it should be (a call's checks are most of
-    # its host time); what is wrong with another one, below
-    if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype)
-            and (shape is None or t.shape == shape) and t.is_contiguous()
-            and (not device or t.is_cuda and t.get_device() == torch._C._cuda_getDevice())):
-        return t.data_ptr()
+def _ptr_checked(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=True,
+                 nullable=False) -> Optional[int]:
+    """_ptr step by step: says what is wrong with a tensor that is not as asked."""
     if t is None:
+        if nullable:
+            return None
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -265,6 +266,24 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=Tr
     return t.data_ptr()
 
 
+# Address of a tensor that has the type, shape, place and layout asked for, in one
+# call; any other goes on to _ptr_checked.
+_ptr = _bind.ptr
+_bind.set_refuse(_ptr_checked)
+
+
+def _cfg_at(cfg: HgaConfig) -> int:
+    if not isinstance(cfg, HgaConfig):
+        raise TypeError(f"cfg must be an HgaConfig, not {type(cfg).__name__}")
+    return ctypes.addressof(cfg)
+
+
+def _axes_at(axes: HgaRopeAxes) -> int:
+    if not isinstance(axes, HgaRopeAxes):
+        raise TypeError(f"axes must be an HgaRopeAxes, not {type(axes).__name__}")
+    return ctypes.addressof(axes)
+
+
 def _check(status: int, where: str) -> None:
     if status != HGA_OK:
         raise HgaError(status, where)
@@ -275,7 +294,7 @@ def apply_rope(cfg: HgaConfig, x: torch.Tensor, x_rot: torch.Tensor, n_outer: in
     shape = (n_outer, n_tokens, n_heads, cfg.head_dim)
     if x.numel() != n_outer * n_tokens * n_heads * cfg.head_dim:
         raise ValueError(f"x must hold {shape} elements")
-    _check(_lib.hga_apply_rope(ctypes.byref(cfg), _ptr(x, "x", cfg.torch_dtype()),
+    _check(_bind.hga_apply_rope(_cfg_at(cfg), _ptr(x, "x", cfg.torch_dtype()),
                                _ptr(x_rot, "x_rot", cfg.torch_dtype(), x.shape), n_outer,
                                n_tokens, n_heads, pos0, _stream(stream)), "hga_apply_rope")
 
@@ -290,8 +309,8 @@ def apply_rope_axes(cfg: HgaConfig, axes: HgaRopeAxes, positions: torch.Tensor, 
     if not isinstance(positions, torch.Tensor) or positions.dim() != 3:
         raise ValueError("positions must be a [n_axes, n_batch, n_tokens] tensor")
     n_batch = positions.shape[1]
-    _check(_lib.hga_apply_rope_axes(
-        ctypes.byref(cfg), ctypes.byref(axes),
+    _check(_bind.hga_apply_rope_axes(
+        _cfg_at(cfg), _axes_at(axes),
         _ptr(positions, "positions", torch.int32, (axes.n_axes, n_batch, n_tokens)),
         _ptr(x, "x", s.dtype), _ptr(x_rot, "x_rot", s.dtype, x.shape),
         n_batch, n_outer, n_tokens, n_heads, _stream(stream)), "hga_apply_rope_axes")
@@ -303,8 +322,8 @@ def build_summaries_axes(cfg: HgaConfig, axes: HgaRopeAxes, positions, k_raw, ch
     B, H, L, d, nC, G = (cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_chunks,
                          cfg.groups_per_chunk)
     dt = cfg.torch_dtype()
-    _check(_lib.hga_build_summaries_axes(
-        ctypes.byref(cfg), ctypes.byref(axes),
+    _check(_bind.hga_build_summaries_axes(
+        _cfg_at(cfg), _axes_at(axes),
         _ptr(positions, "positions", torch.int32, (axes.n_axes, B, L)),
         _ptr(k_raw, "k_raw", dt, (B, H, L, d)),
         _ptr(chunk_sum, "chunk_sum", cfg.summary_torch_dtype(), (B, H, nC, d)),
@@ -324,8 +343,8 @@ def store_kv(cfg: HgaConfig, k, v, k_store, v_store, pos0: int, axes: Optional[H
         raise ValueError("positions need axes")
     n = k.shape[2]
     rows = (c.batch, c.kv_heads, n, c.d)
-    _check(_lib.hga_store_kv(
-        ctypes.byref(cfg), ctypes.byref(axes) if axes is not None else None,
+    _check(_bind.hga_store_kv(
+        _cfg_at(cfg), _axes_at(axes) if axes is not None else None,
         _ptr(positions, "positions", torch.int32,
              (axes.n_axes, c.batch, n) if axes is not None else None, nullable=True),
         _ptr(k, "k", torch.bfloat16, rows), _ptr(v, "v", torch.bfloat16, rows),
@@ -340,8 +359,8 @@ def load_kv(cfg: HgaConfig, k_store, v_store, k, v, pos0: int, stream=None) -> N
         raise ValueError("k must be a [B, Hkv, n, d] tensor")
     n = k.shape[2]
     rows = (c.batch, c.kv_heads, n, c.d)
-    _check(_lib.hga_load_kv(
-        ctypes.byref(cfg), _ptr(k_store, "k_store", c.kv_dtype, c.store),
+    _check(_bind.hga_load_kv(
+        _cfg_at(cfg), _ptr(k_store, "k_store", c.kv_dtype, c.store),
         _ptr(v_store, "v_store", c.kv_dtype, c.store), _ptr(k, "k", torch.bfloat16, rows),
         _ptr(v, "v", torch.bfloat16, rows), int(pos0), n, _stream(stream)), "hga_load_kv")
 
@@ -351,8 +370,8 @@ def build_summaries(cfg: HgaConfig, k_raw, chunk_sum, group_sum, k_rot=None, chu
     B, H, L, d, nC, G = (cfg.batch, cfg.n_kv_heads, cfg.seq_len, cfg.head_dim, cfg.n_chunks,
                          cfg.groups_per_chunk)
     dt = cfg.torch_dtype()
-    _check(_lib.hga_build_summaries(
-        ctypes.byref(cfg), _ptr(k_raw, "k_raw", dt, (B, H, L, d)),
+    _check(_bind.hga_build_summaries(
+        _cfg_at(cfg), _ptr(k_raw, "k_raw", dt, (B, H, L, d)),
         _ptr(chunk_sum, "chunk_sum", cfg.summary_torch_dtype(), (B, H, nC, d)),
         _ptr(group_sum, "group_sum", cfg.summary_torch_dtype(), (B, H, nC * G, d)),
         _ptr(k_rot, "k_rot", dt, (B, H, L, d), nullable=True), int(chunk_begin),
@@ -363,8 +382,8 @@ def route_chunks(cfg: HgaConfig, q_rot, chunk_sum, qbar, sel_chunks, n_sel_chunk
                  stream=None) -> None:
     B, H, d, nQC = cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.n_qchunks
     R = cfg.route_heads
-    _check(_lib.hga_route_chunks(
-        ctypes.byref(cfg), _ptr(q_rot, "q_rot", cfg.torch_dtype(),
+    _check(_bind.hga_route_chunks(
+        _cfg_at(cfg), _ptr(q_rot, "q_rot", cfg.torch_dtype(),
                                 (B, cfg.q_len, cfg.n_q_heads, d)),
         _ptr(chunk_sum, "chunk_sum", cfg.summary_torch_dtype(), (B, H, cfg.n_chunks, d)),
         _ptr(qbar, "qbar", torch.float32, (B, R, nQC, d)),
@@ -378,8 +397,8 @@ def route_groups(cfg: HgaConfig, qbar, group_sum, sel_chunks, n_sel_chunks, sel_
                  n_sel_groups, scores=None, stream=None) -> None:
     B, H, d, nQC, G = cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.n_qchunks, cfg.groups_per_chunk
     R = cfg.route_heads
-    _check(_lib.hga_route_groups(
-        ctypes.byref(cfg), _ptr(qbar, "qbar", torch.float32, (B, R, nQC, d)),
+    _check(_bind.hga_route_groups(
+        _cfg_at(cfg), _ptr(qbar, "qbar", torch.float32, (B, R, nQC, d)),
         _ptr(group_sum, "group_sum", cfg.summary_torch_dtype(), (B, H, cfg.n_chunks * G, d)),
         _ptr(sel_chunks, "sel_chunks", torch.int32, (B, R, nQC, cfg.top_k_chunks)),
         _ptr(n_sel_chunks, "n_sel_chunks", torch.int32, (B, R, nQC)),
@@ -410,7 +429,7 @@ def route(cfg: HgaConfig, q_rot, chunk_sum, group_sum, qbar, sel_chunks, n_sel_c
     """Both routing levels (one launch for a one-token span)."""
     args = _route_ptrs(cfg, q_rot, chunk_sum, group_sum, qbar, sel_chunks, n_sel_chunks,
                        sel_groups, n_sel_groups)
-    _check(_lib.hga_route(ctypes.byref(cfg), *args, _stream(stream)), "hga_route")
+    _check(_bind.hga_route(_cfg_at(cfg), *args, _stream(stream)), "hga_route")
 
 
 def decode_step(cfg: HgaConfig, q_rot, chunk_sum, group_sum, k_cache, v_cache, qbar, sel_chunks,
@@ -420,8 +439,8 @@ def decode_step(cfg: HgaConfig, q_rot, chunk_sum, group_sum, k_cache, v_cache, q
     dt, kvt, store = cfg.torch_dtype(), cfg.kv_torch_dtype(), cfg.kv_rows(B, H, rows=L)
     r = _route_ptrs(cfg, q_rot, chunk_sum, group_sum, qbar, sel_chunks, n_sel_chunks, sel_groups,
                     n_sel_groups)
-    _check(_lib.hga_decode_step(
-        ctypes.byref(cfg), r[0], r[1], r[2],
+    _check(_bind.hga_decode_step(
+        _cfg_at(cfg), r[0], r[1], r[2],
         _ptr(k_cache, "k_cache", kvt, store), _ptr(v_cache, "v_cache", kvt, store),
         *r[3:], _ptr(out, "out", dt, (B, cfg.q_len, cfg.n_q_heads, d)), _stream(stream)),
         "hga_decode_step")
@@ -438,8 +457,8 @@ def decode_step_tiered(cfg: HgaConfig, q_rot, chunk_sum, group_sum, k_win, v_win
     store = cfg.kv_rows(B, H, rows=L)
     r = _route_ptrs(cfg, q_rot, chunk_sum, group_sum, qbar, sel_chunks, n_sel_chunks, sel_groups,
                     n_sel_groups)
-    _check(_lib.hga_decode_step_tiered(
-        ctypes.byref(cfg), r[0], r[1], r[2], _ptr(k_win, "k_win", kvt, win),
+    _check(_bind.hga_decode_step_tiered(
+        _cfg_at(cfg), r[0], r[1], r[2], _ptr(k_win, "k_win", kvt, win),
         _ptr(v_win, "v_win", kvt, win), _ptr(k_host, "k_host", kvt, store, device=False),
         _ptr(v_host, "v_host", kvt, store, device=False), *r[3:],
         _ptr(out, "out", dt, (B, cfg.q_len, cfg.n_q_heads, d)), _stream(stream)),
@@ -452,8 +471,8 @@ def gather_kv(cfg: HgaConfig, k_src, v_src, src_is_host: bool, sel_groups, n_sel
     dt = cfg.kv_torch_dtype()
     dst_shape = cfg.kv_rows(B, H, nQC, rows=cfg.top_k_groups * cfg.group_size)
     store = cfg.kv_rows(B, H, rows=L)
-    _check(_lib.hga_gather_kv(
-        ctypes.byref(cfg), _ptr(k_src, "k_src", dt, store, device=not src_is_host),
+    _check(_bind.hga_gather_kv(
+        _cfg_at(cfg), _ptr(k_src, "k_src", dt, store, device=not src_is_host),
         _ptr(v_src, "v_src", dt, store, device=not src_is_host), int(bool(src_is_host)),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, H, nQC, cfg.top_k_groups)),
         _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, H, nQC)),
@@ -471,8 +490,8 @@ def gather_kv_warm(cfg: HgaConfig, k_host, v_host, sel_groups, n_sel_groups, poo
     store = cfg.kv_rows(B, H, rows=cfg.seq_len)
     gat_shape = cfg.kv_rows(B, H, cfg.n_qchunks, rows=kg * g)
     pool = pool_shape(cfg, n_slots)
-    _check(_lib.hga_gather_kv_warm(
-        ctypes.byref(cfg), _ptr(k_host, "k_host", dt, store, device=False),
+    _check(_bind.hga_gather_kv_warm(
+        _cfg_at(cfg), _ptr(k_host, "k_host", dt, store, device=False),
         _ptr(v_host, "v_host", dt, store, device=False),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, H, cfg.n_qchunks, kg)),
         _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, H, cfg.n_qchunks)),
@@ -497,8 +516,8 @@ def gather_kv_warm_noalloc(cfg: HgaConfig, k_host, v_host, sel_groups, n_sel_gro
     store = cfg.kv_rows(B, H, rows=cfg.seq_len)
     gat_shape = cfg.kv_rows(B, H, cfg.n_qchunks, rows=kg * g)
     pool = pool_shape(cfg, n_slots)
-    _check(_lib.hga_gather_kv_warm_noalloc(
-        ctypes.byref(cfg), _ptr(k_host, "k_host", dt, store, device=False),
+    _check(_bind.hga_gather_kv_warm_noalloc(
+        _cfg_at(cfg), _ptr(k_host, "k_host", dt, store, device=False),
         _ptr(v_host, "v_host", dt, store, device=False),
         _ptr(sel_groups, "sel_groups", torch.int32, (B, H, cfg.n_qchunks, kg)),
         _ptr(n_sel_groups, "n_sel_groups", torch.int32, (B, H, cfg.n_qchunks)),
@@ -525,8 +544,8 @@ def window_slots(cfg: HgaConfig) -> int:
 def attend(cfg: HgaConfig, q_rot, k_res, v_res, sel_groups, n_sel_groups, out, k_gat=None,
            v_gat=None, stream=None) -> None:
     c = _shapes(cfg)
-    _check(_lib.hga_attend(
-        ctypes.byref(cfg), _ptr(q_rot, "q_rot", c.dtype, c.q),
+    _check(_bind.hga_attend(
+        _cfg_at(cfg), _ptr(q_rot, "q_rot", c.dtype, c.q),
         _ptr(k_res, "k_res", c.kv_dtype, c.res), _ptr(v_res, "v_res", c.kv_dtype, c.res),
         _ptr(k_gat, "k_gat", c.kv_dtype, c.gathered, nullable=True),
         _ptr(v_gat, "v_gat", c.kv_dtype, c.gathered, nullable=True),
