@@ -117,7 +117,8 @@ cudaError_t launch_attend_tc_pages(const Params& p, const void* q_rot, const KvS
                                    void* out, cudaStream_t st);
 
 // True when the cluster / MMA decode kernels cover this configuration (bf16,
-// d = 128, one query token, gq <= 8, and L % 16 == 0 or the 4-bit store).
+// d = 128, one query token, gq <= 8 and L % 16 == 0; over the 4-bit store any L, and
+// short spans token by token).
 bool decode_kernel_supports(const Params& p);
 
 cudaError_t launch_attend_decode(const Params& p, const void* q_rot, const KvSources& kv,

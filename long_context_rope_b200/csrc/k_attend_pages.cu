@@ -1,12 +1,12 @@
-// k_attend_pages.cu -- single-token (decode) exact attention over the routed set
-// of a 4-bit store (HGA_KV_E2M1).
+// k_attend_pages.cu -- exact attention of single tokens over the routed set of a
+// 4-bit store (HGA_KV_E2M1): a decode step, or a span of few tokens.
 //
 // "Technische Samenvatting: Hierarchical Global Attention (HGA)"
 // (gist.science), "Kernmechanisme" item 4: standard softmax over the bounded
 // exact token set. Every page of the set is read once (2304 bytes for 16 keys
 // and values), and the query heads of a KV head share each load (GQA).
 //
-// One cluster of CL CTAs of four warps per (sequence, KV head): CL as large as
+// One cluster of CL CTAs of four warps per unit (token, sequence, KV head): CL as large as
 // keeps every unit's cluster resident at once (four CTAs per SM), and no larger
 // than gives every warp a page. Block i of the unit (forced blocks, then the
 // routed list) goes to warp i mod 4 CL of the cluster, and each warp works out
@@ -39,20 +39,20 @@ struct PagesSmem : dec::PageSmem<kWarps> {
                                                     // gathered buffer), first position
 };
 
-// The keys' chunks that are always visible, up to the query's block: sinks
-// [0, s_end), then [l_begin, j].
+// The keys' chunks that are always visible to position qpos, up to its block:
+// sinks [0, s_end), then [l_begin, j].
 struct Forced {
     int s_end, l_begin, blocks;
 };
 
-__host__ __device__ __forceinline__ Forced forced_of(const Params& p) {
+__host__ __device__ __forceinline__ Forced forced_of(const Params& p, int qpos) {
     Forced f;
-    const int j = p.j0;
+    const int j = qpos / p.C;
     f.s_end = p.n_sink < j + 1 ? p.n_sink : j + 1;
     f.l_begin = j - p.n_local > f.s_end ? j - p.n_local : f.s_end;
     // chunk j comes last; with a sink chunk j it is [0, s_end)'s
     const int chunks = f.s_end + (j + 1 - f.l_begin);
-    f.blocks = (chunks - 1) * p.G + (int)((p.q_begin - (int64_t)j * p.C) / kGroupRows) + 1;
+    f.blocks = (chunks - 1) * p.G + (qpos - j * p.C) / kGroupRows + 1;
     return f;
 }
 
@@ -67,20 +67,25 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) attend_pages_kernel(
     ptx::cluster_started_arrive();
     const int CL = (int)cluster.num_blocks(), r = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t bh = blockIdx.y;  // routing unit: (sequence, KV head) or (sequence, query head)
+    const int tok = blockIdx.y / (p.B * p.Hu);
+    // routing unit: (sequence, KV head) or (sequence, query head)
+    const int64_t bh = blockIdx.y - tok * (p.B * p.Hu);
     const int b = (int)(bh / p.Hu), h = (int)(bh % p.Hu);
     const int64_t kvh = (int64_t)b * p.Hkv + h / (p.Hu / p.Hkv);  // its K/V row
-    const int j = p.j0;
+    const int qpos = p.q_begin + tok, j = qpos / p.C;
+    const int64_t prob = bh * p.nQC + (j - p.j0);
+    q += (int64_t)tok * p.Hq * dec::kD;
+    out += (int64_t)tok * p.Hq * dec::kD;
     const bool gathered = gat.k != nullptr;
 
     // ---- this warp's blocks; the count and the first 32 entries in one round trip
-    const Forced f = forced_of(p);
+    const Forced f = forced_of(p, qpos);
     const int first = warp * CL + r, step = kWarps * CL;
-    const int32_t* list = sel + bh * p.kg;
+    const int32_t* list = sel + prob * p.kg;
     auto entry = [&](int s) { return s >= 0 && s < p.kg ? list[s] : -1; };
     int s = first + step * lane - f.blocks;
     int gi = entry(s), prev = entry(s - 1);
-    int n_list = nsel[bh];
+    int n_list = nsel[prob];
     uint32_t qf[8][2];
     float sc[2];
     dec::load_q_pages(p, q, b, h, qf, sc);
@@ -120,9 +125,9 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) attend_pages_kernel(
     dec::WarpAcc acc;
     dec::acc_init(acc);
     const dec::PageRef rbase = dec::lane_pages(res.k + kvh * res.slab, res.v + kvh * res.slab);
-    const dec::PageRef gbase = dec::lane_pages(gat.k + bh * gat.slab, gat.v + bh * gat.slab);
+    const dec::PageRef gbase = dec::lane_pages(gat.k + prob * gat.slab, gat.v + prob * gat.slab);
     dec::consume_pages(
-        qf, sc, sm.u.page[warp], n, p.q_begin,
+        qf, sc, sm.u.page[warp], n, qpos,
         [&](int i) {
             const int page = sm.blk[warp][i].x;
             return dec::page_at((page & kSrcGathered) ? gbase : rbase, page & ~kSrcGathered);
@@ -194,8 +199,8 @@ cudaError_t launch_attend_pages(const Params& p, const void* q_rot, const KvSour
                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t units = (int64_t)p.B * p.Hu;
-    const int blocks = forced_of(p).blocks + p.kg;
+    const int64_t units = (int64_t)p.q_len * p.B * p.Hu;
+    const int blocks = forced_of(p, p.q_begin + p.q_len - 1).blocks + p.kg;
     int64_t most = (int64_t)kCtasPerSm * sms / units;
     if (most > (blocks + kWarps - 1) / kWarps) most = (blocks + kWarps - 1) / kWarps;
     most = most < 1 ? 1 : (most > kMaxCluster ? kMaxCluster : most);

@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 
 bool tc_kernel_supports(const Params& p, bool gathered) {
     if (gathered || p.kv_layout != HGA_KV_FULL) return false;
-    // a decode step of more than 8 heads, which the decode kernels do not take, too
-    if (p.kv_f4) return p.gq <= kRows && (p.q_len > 1 || p.gq > 8);
+    // what the kernel of single tokens does not take: longer spans, more than 8 heads
+    if (p.kv_f4) return p.gq <= kRows && !decode_kernel_supports(p);
     return p.q_len > 1 && p.dtype == HGA_BF16 && p.d == kD && p.gq == 8 && p.C % 32 == 0;
 }
 

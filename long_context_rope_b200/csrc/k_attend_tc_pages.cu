@@ -32,6 +32,8 @@
 // last 16K tokens of 32K in 508 to 527 us (898 to 931 TFLOP/s), 4K tokens in 113
 // to 119 us.
 //
+// Spans of few tokens (at most 8 heads per KV head) go to k_attend_pages.cu.
+//
 // An M tile holds 128 / gq whole tokens (all gq heads of each), so any number
 // of query heads per KV head up to 128 is served; rows past that are idle.
 //

@@ -817,3 +817,35 @@ def test_append_on_another_stream(kv4, handle):
         outs.append(got)
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+# spans around the 592 units (tokens x sequences x KV heads) up to which they go token by
+# token, on either side; chunks and query blocks that begin and end inside a span
+SPANS = [dict(q_begin=100, q_len=592, seq_len=700), dict(q_begin=100, q_len=593, seq_len=700),
+         dict(q_begin=61, q_len=148, seq_len=209, n_kv_heads=2, n_q_heads=16, batch=2),
+         dict(q_begin=61, q_len=149, seq_len=215, n_kv_heads=2, n_q_heads=16, batch=2),
+         dict(q_begin=500, q_len=3, seq_len=520, n_kv_heads=4, n_q_heads=12, batch=3),
+         dict(q_begin=63, q_len=2, seq_len=200, n_sink=0, n_local=0),
+         dict(q_begin=40, q_len=700, seq_len=740, n_q_heads=3),
+         dict(q_begin=40, q_len=300, seq_len=345, n_q_heads=2, n_kv_heads=1, batch=2),
+         dict(q_begin=0, q_len=320, seq_len=320, batch=2, n_sink=2, n_local=0),
+         dict(q_begin=190, q_len=220, seq_len=420, chunk_size=48, groups_per_chunk=3, batch=3)]
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("kw", SPANS, ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_attend_spans(kw, gathered):
+    """Short and long spans of queries, from the store or from gathered groups."""
+    from long_context_rope_b200 import hga, pipeline
+    cfg = _cfg4(hga, **kw)
+    q, kp, vp, sel, n, want, tol = _attend_case(hga, cfg, 96)
+    q, kp, vp, sel, n = (x.cuda() for x in (q, kp, vp, sel, n))
+    out = torch.full(q.shape, float("nan"), dtype=BF, device="cuda")
+    gat = {}
+    if gathered:
+        kg, vg = pipeline.alloc_gathered(cfg)
+        hga.gather_kv(cfg, kp, vp, False, sel, n, kg, vg)
+        gat = dict(k_gat=kg, v_gat=vg)
+    hga.attend(cfg, q, kp, vp, sel, n, out, **gat)
+    _clean(hga)
+    _check(out, want, tol)
