@@ -849,3 +849,25 @@ def test_attend_spans(kw, gathered):
     hga.attend(cfg, q, kp, vp, sel, n, out, **gat)
     _clean(hga)
     _check(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (torch.float32, 128), (BF, 64), (torch.float32, 64)])
+@pytest.mark.parametrize("rep,heads,T", [(1, 1, 9001), (4, 1, 7659), (1, 5, 12007), (3, 2, 5003), (1, 9, 6001)])
+def test_rope_of_few_rows_equals_its_parts(dtype, d, rep, heads, T):
+    """Many tokens of few rows each: how rows fall to threads changes with the size of the
+    call, their values do not."""
+    from long_context_rope_b200 import hga
+    B = 2
+    cfg = _cfg(hga, batch=B, head_dim=d, n_high_freq_pairs=0, dtype="bf16" if dtype == BF else "f32")
+    axes = hga.rope_axes(hga.pair_axes(d // 2, [d // 4, d // 8]), 2)
+    g = torch.Generator().manual_seed(T)
+    pos = torch.randint(-100, 1 << 18, (2, B, T), generator=g, dtype=torch.int32).cuda()
+    x = torch.randn(B * rep, T, heads, d, generator=g).to(dtype).cuda()
+    y = torch.full_like(x, float("nan"))
+    hga.apply_rope_axes(cfg, axes, pos, x, y, B * rep, T, heads)
+    for a, b in ((0, 37), (T // 2, T // 2 + 40), (T - 29, T)):
+        part = x[:, a:b].contiguous()
+        got = torch.empty_like(part)
+        hga.apply_rope_axes(cfg, axes, pos[:, :, a:b].contiguous(), part, got, B * rep, b - a, heads)
+        assert torch.equal(y[:, a:b], got)
+    _clean(hga)
