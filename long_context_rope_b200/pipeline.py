@@ -104,11 +104,28 @@ def _check_axes(axes, positions, shape) -> None:
                          f"got {tuple(positions.shape)}")
 
 
+def _as_stream(stream) -> torch.cuda.Stream:
+    """A stream given as torch's object or as its handle."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
+def _aligned(positions: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
+    """Positions at an address that the calls take. One axis of one sequence from some
+    token on is contiguous as it lies, wherever it starts: it is copied, on `stream`."""
+    if positions is None or positions.data_ptr() % 16 == 0:
+        return positions
+    if stream is None or not positions.is_cuda:
+        return positions.clone()
+    with torch.cuda.stream(_as_stream(stream)):
+        return positions.clone()
+
+
 def rotate_queries(cfg: hga.HgaConfig, q_raw: torch.Tensor, stream=None, axes=None,
                    positions=None) -> torch.Tensor:
     """Rotate queries [B, q_len, Hq, d] by their token positions, or with axes by
     positions [n_axes, B, q_len] int32."""
     _check_axes(axes, positions, (cfg.batch, cfg.q_len))
+    positions = _aligned(positions, stream)
     q_rot = torch.empty_like(q_raw)
     if axes is not None:
         hga.apply_rope_axes(cfg, axes, positions, q_raw, q_rot, cfg.batch, cfg.q_len, cfg.n_q_heads,
@@ -123,6 +140,7 @@ def summaries(cfg: hga.HgaConfig, k_raw, cs, gs, k_rot=None, stream=None, axes=N
     """Key summaries (and rotated keys) of chunks [chunk_begin, chunk_end), by token
     position or with axes by positions [n_axes, B, L] int32."""
     _check_axes(axes, positions, (cfg.batch, cfg.seq_len))
+    positions = _aligned(positions, stream)
     chunk_end = cfg.n_chunks if chunk_end is None else chunk_end
     if axes is not None:
         hga.build_summaries_axes(cfg, axes, positions, k_raw, cs, gs, k_rot, chunk_begin, chunk_end,
@@ -159,6 +177,8 @@ def prefill(cfg: hga.HgaConfig, k_raw, v, q_rot, cs, gs, k_rot, rb: RouteBuffers
     With kv_type E2M1, k_rot and v_store are the 4-bit stores, which the pass
     fills (hga_store_kv, the keys rotated on the way) and attends over. axes
     and positions [n_axes, B, L]: rotary positions with several axes."""
+    _check_axes(axes, positions, (cfg.batch, cfg.seq_len))
+    positions = _aligned(positions, stream)
     if cfg.kv_type == hga.HGA_KV_E2M1:
         summaries(cfg, k_raw, cs, gs, None, stream, axes, positions)
         hga.store_kv(cfg, k_raw, v, k_rot, v_store, 0, axes or _one_axis(cfg), positions, stream)
@@ -227,11 +247,6 @@ def fill_windows(cfg: hga.HgaConfig, k_full, v_full, k_win, v_win):
         v_win[:, :, w * C: w * C + hi - c * C].copy_(v_full[:, :, c * C: hi], non_blocking=True)
 
 
-def _as_stream(stream) -> torch.cuda.Stream:
-    """A stream given as torch's object or as its handle."""
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-
-
 def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new, k_raw_cache,
                   k_rot_cache, v_cache, cs, gs, rb: RouteBuffers, out, stream=None, axes=None,
                   positions=None):
@@ -259,7 +274,7 @@ def decode_append(cfg_cap: hga.HgaConfig, pos: int, k_new_raw, v_new, q_rot_new,
     B, H, d = cfg_cap.batch, cfg_cap.n_kv_heads, cfg_cap.head_dim
     _check_axes(axes, positions, (B, cfg_cap.seq_len))
     k_new_raw = k_new_raw.contiguous()
-    at = None if positions is None else positions[:, :, pos:pos + 1].contiguous()
+    at = None if positions is None else _aligned(positions[:, :, pos:pos + 1].contiguous(), stream)
     k_raw_cache[:, :, pos].copy_(k_new_raw, non_blocking=True)
     rot_cache = k_rot_cache
     if cfg_cap.kv_type == hga.HGA_KV_E2M1:
