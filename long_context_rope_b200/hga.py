@@ -130,12 +130,12 @@ def rope_axes(pair_axis, n_axes: int, inverse: bool = False) -> HgaRopeAxes:
 
 
 class _Shapes:
-    """What calls of one configuration ask of their tensors."""
+    """What calls of one configuration ask of their tensors; n_qchunks: of its span."""
 
-    def __init__(self, c: HgaConfig):
+    def __init__(self, c: HgaConfig, n_qchunks: int):
         if c.chunk_size < 1 or c.groups_per_chunk < 1:
             raise HgaError(-8, "configuration")
-        B, H, L, d, nQC, R = (c.batch, c.n_kv_heads, c.seq_len, c.head_dim, c.n_qchunks,
+        B, H, L, d, nQC, R = (c.batch, c.n_kv_heads, c.seq_len, c.head_dim, n_qchunks,
                               c.route_heads)
         self.batch, self.kv_heads, self.d = B, H, d
         self.dtype, self.kv_dtype = c.torch_dtype(), c.kv_torch_dtype()
@@ -147,14 +147,24 @@ class _Shapes:
         self.sel, self.n_sel = (B, R, nQC, c.top_k_groups), (B, R, nQC)
 
 
+_AT_L, _AT_Q = HgaConfig.seq_len.offset, HgaConfig.q_begin.offset
+
+
 @functools.lru_cache(maxsize=256)
-def _shapes_of(fields: bytes) -> _Shapes:
-    return _Shapes(HgaConfig.from_buffer_copy(fields))
+def _shapes_of(fields: bytes, n_qchunks: int) -> _Shapes:
+    """fields: a configuration's bytes, q_begin left out."""
+    return _Shapes(HgaConfig.from_buffer_copy(fields[:_AT_Q] + bytes(4) + fields[_AT_Q:]), n_qchunks)
 
 
-def _shapes(cfg: HgaConfig) -> _Shapes:
-    """By the configuration's values, so that a decode loop works them out once."""
-    return _shapes_of(bytes(cfg))
+def _shapes(cfg: HgaConfig, windows: bool = False) -> _Shapes:
+    """By the configuration's values, so that a decode loop works them out once: where
+    its one query stands is not among them, nor, for a call that reads windows, how
+    long the context is (its `store` is then not to be used)."""
+    fields = bytes(cfg)
+    if windows:
+        fields = fields[:_AT_L] + bytes(4) + fields[_AT_L + 4:]
+    return _shapes_of(fields[:_AT_Q] + fields[_AT_Q + 4:],
+                      1 if cfg.q_len == 1 or cfg.chunk_size < 1 else cfg.n_qchunks)
 
 
 def _load():
@@ -543,7 +553,7 @@ def window_slots(cfg: HgaConfig) -> int:
 
 def attend(cfg: HgaConfig, q_rot, k_res, v_res, sel_groups, n_sel_groups, out, k_gat=None,
            v_gat=None, stream=None) -> None:
-    c = _shapes(cfg)
+    c = _shapes(cfg, windows=cfg.kv_layout == HGA_KV_WINDOWS)
     _check(_bind.hga_attend(
         _cfg_at(cfg), _ptr(q_rot, "q_rot", c.dtype, c.q),
         _ptr(k_res, "k_res", c.kv_dtype, c.res), _ptr(v_res, "v_res", c.kv_dtype, c.res),
