@@ -32,6 +32,15 @@ __device__ __forceinline__ void codes_to_f16x2(uint32_t w, uint32_t (&f)[4]) {
         : "r"(w));
 }
 
+// v * ts cut to fp32, its last bit set where anything was cut off: rounded on to bf16
+// that is the product rounded once. (A product rounded to fp32 first may come to lie
+// halfway between two bf16 numbers, and then go the wrong way.)
+__device__ __forceinline__ float mul_to_odd(float v, float ts) {
+    const float q = __fmul_rz(v, ts);
+    const bool cut = __fmaf_ru(fabsf(v), ts, -fabsf(q)) > 0.f;  // rounded up: never lost
+    return __uint_as_float(__float_as_uint(q) | (cut ? 1u : 0u));
+}
+
 // Eight floats to codes, nearest even, at most 6 in magnitude.
 __device__ __forceinline__ uint32_t f32x8_to_codes(const float* q) {
     uint32_t w;

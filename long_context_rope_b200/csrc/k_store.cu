@@ -12,6 +12,8 @@
 // element (a correctly rounded quotient in three). 64K tokens x 4 heads (172
 // MB each way): written in 38 us, bound by instructions; read back in 28.5 us,
 // 0.92 of the copy bandwidth.
+#include <string.h>
+
 #include "hga_e2m1.cuh"
 #include "hga_kernels.h"
 #include "hga_turn.cuh"
@@ -187,9 +189,11 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(
 }
 
 // grid.y = 0: keys, 1: values. Item = (row, 8 dims): row * 16 + piece; a
-// thread has kLoadItems of them in flight, a grid apart.
+// thread has kLoadItems of them in flight, a grid apart. kExact: code x block scale
+// times either tensor scale is an fp32 number.
 constexpr int kLoadItems = 4;
 
+template <bool kExact>
 __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
     const __grid_constant__ Params p, const uint8_t* __restrict__ ks,
     const uint8_t* __restrict__ vs, bf* __restrict__ k, bf* __restrict__ v, int pos0,
@@ -230,8 +234,8 @@ __global__ void __launch_bounds__(kStoreThreads) load_kv_kernel(
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t h = e2m1::hmul2(f[e], s2);
                     const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                    o[2 * e] = r.x * ts;
-                    o[2 * e + 1] = r.y * ts;
+                    o[2 * e] = kExact ? r.x * ts : e2m1::mul_to_odd(r.x, ts);
+                    o[2 * e + 1] = kExact ? r.y * ts : e2m1::mul_to_odd(r.y, ts);
                 }
                 *reinterpret_cast<uint4*>(dst + dst_row[i] * 128 + 8 * pc) = f32x8_to_bf16(o);
             }
@@ -259,11 +263,21 @@ cudaError_t launch_store_kv(const Params& p, const AxisMap& am, const int32_t* p
     });
 }
 
+// Code x block scale has 6 significant bits and is 2^-10 at least, so 18 bits of a
+// tensor scale far above fp32's smallest are exact.
+static bool exact_scale(float ts) {
+    uint32_t bits;
+    memcpy(&bits, &ts, sizeof(bits));
+    return (bits & 0x3fu) == 0u && ts > 0x1p-100f;
+}
+
 cudaError_t launch_load_kv(const Params& p, const void* k_store, const void* v_store, void* k,
                            void* v, int64_t pos0, int64_t n_tokens, cudaStream_t st) {
+    auto* kernel = exact_scale(p.k_scale) && exact_scale(p.v_scale) ? load_kv_kernel<true>
+                                                                    : load_kv_kernel<false>;
     return each_launch((int64_t)p.B * p.Hkv, n_tokens, [&](const Rows& rows) {
         const int64_t threads = ((int64_t)rows.n * 16 + kLoadItems - 1) / kLoadItems;
-        load_kv_kernel<<<dim3(grid_of(threads), 2), kStoreThreads, 0, st>>>(
+        kernel<<<dim3(grid_of(threads), 2), kStoreThreads, 0, st>>>(
             p, (const uint8_t*)k_store, (const uint8_t*)v_store, (bf*)k, (bf*)v, (int)pos0, rows);
     });
 }

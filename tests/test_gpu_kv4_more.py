@@ -45,3 +45,39 @@ def test_append_one_axis_of_one_sequence(kv4):
     all_q = torch.empty(1, L, 16, 128, dtype=BF, device="cuda")
     hga.apply_rope_axes(cfg, axes, pos, q.expand(1, L, 16, 128).contiguous(), all_q, 1, L, 16)
     assert torch.equal(torch.cat(turned, 1), all_q)
+
+
+def _to_bf16(x):
+    """64-bit numbers rounded once to bf16 (nearest even), as 64-bit numbers."""
+    _, e = torch.frexp(x)
+    step = torch.ldexp(torch.ones_like(x), e.clamp(min=-125) - 8)   # 8 bits; subnormals below 2^-126
+    r = torch.round(x / step) * step
+    return torch.where(r.abs() >= 2.0 ** 128, torch.copysign(torch.full_like(r, float("inf")), r), r)
+
+
+# scales under which a product rounded to fp32 first becomes a tie between two bf16 numbers and
+# goes the wrong way; ordinary ones; those near fp32's ends
+@pytest.mark.parametrize("scale", [float.fromhex(s) for s in (
+    "0x1.e6aaacp-9", "0x1.45b6dcp-9", "0x1.5c924ap-9", "0x1.b364dap-9", "0x1.18e38ep-9", "0x1.18e38ep-99",
+    "0x1.45b6dcp-101", "0x1.b364dap-126", "0x1.18e38p-130", "0x1p-149", "0x1p-8", "0x1.8p-8", "0x1.333334p-2",
+    "0x1.e6aaacp+40", "0x1.b364dap+125", "0x1.fffffep+127")])
+def test_load_rounds_once(scale):
+    """Every code under every scale byte."""
+    from long_context_rope_b200 import hga
+    ts = float(torch.tensor(scale, dtype=torch.float32))
+    assert ts == scale
+    cfg = _cfg4(hga, seq_len=32, k_scale=scale, v_scale=1.0)
+    code = (torch.arange(32 * 128) % 16).to(torch.uint8).view(1, 1, 32, 128)
+    byte = torch.arange(256).to(torch.uint8).view(1, 1, 32, 8)
+    pages = R.pack(code, byte)
+    want = _to_bf16(R.values(pages, ts))
+    k = torch.empty(1, 1, 32, 128, dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    p = pages.cuda()
+    hga.load_kv(cfg, p, p, k, v, 0)
+    _clean(hga)
+    got, nan = k.cpu().double(), torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
+    assert torch.equal(torch.signbit(got[~nan]), torch.signbit(want[~nan]))
+    v = v.cpu().double()
+    assert torch.equal(v[~nan], R.values(pages, 1.0)[~nan])
