@@ -6,6 +6,8 @@
 // ptr(t, name, dtype=None, shape=None, device=True, nullable=False): the tensor's
 // address if it is as asked; whatever else goes on to the Python function given
 // to set_refuse, which finds out what is wrong and raises.
+// shape_key(cfg, windows): the bytes of the hga_config at address cfg, but in the place of
+// q_begin the number of chunks that the span touches, and with windows seq_len 0.
 // hga_*(...): as declared in hga.h; pointers are integers or None.
 #include <Python.h>
 
@@ -87,6 +89,23 @@ PyObject* set_refuse(PyObject*, PyObject* f) {
     Py_RETURN_NONE;
 }
 
+PyObject* shape_key(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 2) return PyErr_Format(PyExc_TypeError, "2 arguments, not %zd", n);
+    const auto* at = static_cast<const hga_config*>(PyLong_AsVoidPtr(args[0]));
+    if (!at) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no configuration");
+        return nullptr;
+    }
+    PyObject* out = PyBytes_FromStringAndSize(reinterpret_cast<const char*>(at), sizeof(*at));
+    if (!out) return nullptr;
+    auto* c = reinterpret_cast<hga_config*>(PyBytes_AS_STRING(out));
+    const int64_t first = c->q_begin, last = first + c->q_len - 1, size = c->chunk_size;
+    auto chunk = [size](int64_t t) { return t / size - (t % size < 0 ? 1 : 0); };
+    c->q_begin = c->q_len < 1 || size < 1 ? 0 : (int32_t)(chunk(last) - chunk(first) + 1);
+    if (args[1] == Py_True) c->seq_len = 0;
+    return out;
+}
+
 template <typename T>
 bool get(PyObject* o, T*& v) {
     v = nullptr;
@@ -134,6 +153,8 @@ PyMethodDef g_methods[] = {
     {"ptr", (PyCFunction)(void (*)(void))ptr, METH_FASTCALL | METH_KEYWORDS,
      "Address of a tensor that has the type, shape, place and layout asked for."},
     {"set_refuse", set_refuse, METH_O, "What ptr goes on to for any other argument."},
+    {"shape_key", (PyCFunction)(void (*)(void))shape_key, METH_FASTCALL,
+     "A configuration's bytes, the same wherever its span of as many chunks lies."},
     HGA_ENTRY(hga_apply_rope),
     HGA_ENTRY(hga_apply_rope_axes),
     HGA_ENTRY(hga_build_summaries),

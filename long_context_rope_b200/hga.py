@@ -147,24 +147,18 @@ class _Shapes:
         self.sel, self.n_sel = (B, R, nQC, c.top_k_groups), (B, R, nQC)
 
 
-_AT_L, _AT_Q = HgaConfig.seq_len.offset, HgaConfig.q_begin.offset
-
-
 @functools.lru_cache(maxsize=256)
-def _shapes_of(fields: bytes, n_qchunks: int) -> _Shapes:
-    """fields: a configuration's bytes, q_begin left out."""
-    return _Shapes(HgaConfig.from_buffer_copy(fields[:_AT_Q] + bytes(4) + fields[_AT_Q:]), n_qchunks)
+def _shapes_of(fields: bytes) -> _Shapes:
+    """fields: as _bind.shape_key gives them, the span's chunks in the place of q_begin."""
+    c = HgaConfig.from_buffer_copy(fields)
+    return _Shapes(c, c.q_begin)
 
 
 def _shapes(cfg: HgaConfig, windows: bool = False) -> _Shapes:
     """By the configuration's values, so that a decode loop works them out once: where
     its one query stands is not among them, nor, for a call that reads windows, how
     long the context is (its `store` is then not to be used)."""
-    fields = bytes(cfg)
-    if windows:
-        fields = fields[:_AT_L] + bytes(4) + fields[_AT_L + 4:]
-    return _shapes_of(fields[:_AT_Q] + fields[_AT_Q + 4:],
-                      1 if cfg.q_len == 1 or cfg.chunk_size < 1 else cfg.n_qchunks)
+    return _shapes_of(_bind.shape_key(_cfg_at(cfg), windows))
 
 
 def _load():

@@ -48,3 +48,20 @@ def test_what_the_shapes_depend_on_tells_them_apart(hga):
     for bad in (dict(chunk_size=0), dict(groups_per_chunk=0), dict(chunk_size=0, q_len=1)):
         with pytest.raises(hga.HgaError):
             hga._shapes(base.copy(**bad))
+
+
+def test_key_counts_the_chunks_of_a_span(hga):
+    import ctypes
+    import random
+    rng = random.Random(5)
+    for _ in range(300):
+        c = _cfg(hga, q_begin=rng.choice((0, 1, 63, 64, rng.randrange(4096))),
+                 q_len=rng.choice((0, 1, 2, 64, 65, rng.randrange(500))))
+        key = hga.HgaConfig.from_buffer_copy(hga._bind.shape_key(ctypes.addressof(c), False))
+        assert key.q_begin == c.n_qchunks
+        back = key.copy(q_begin=c.q_begin)
+        assert all(getattr(back, n) == getattr(c, n) for n, _ in c._fields_)
+    with pytest.raises(ValueError):
+        hga._bind.shape_key(None, False)
+    with pytest.raises(TypeError):
+        hga._bind.shape_key(5)
