@@ -62,6 +62,7 @@ def test_key_counts_the_chunks_of_a_span(hga):
         back = key.copy(q_begin=c.q_begin)
         assert all(getattr(back, n) == getattr(c, n) for n, _ in c._fields_)
     with pytest.raises(ValueError):
-        hga._bind.shape_key(None, False)
-    with pytest.raises(TypeError):
-        hga._bind.shape_key(5)
+        hga._bind.shape_key(0, False)
+    for args in ((None, False), (5,)):
+        with pytest.raises(TypeError):
+            hga._bind.shape_key(*args)
