@@ -2,7 +2,8 @@
 
 Each CUDA source under csrc/ is compiled to an object in _build/ (in
 parallel), then linked into long_context_rope_b200/libhga.so; csrc/py_bind.cpp
-becomes long_context_rope_b200/_hga_bind.so, which links to it. Run as
+becomes long_context_rope_b200/_hga_bind.so, which links to it. The binding reads
+torch's own objects, so another version of torch or Python builds it again. Run as
 ``python -m long_context_rope_b200.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -24,6 +26,7 @@ OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhga.so")
 BIND = os.path.join(PKG, "_hga_bind.so")
 BIND_SRC = os.path.join(CSRC, "py_bind.cpp")
+BIND_FOR = os.path.join(OUT_DIR, "_hga_bind.for")  # what BIND was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -84,17 +87,35 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link of libhga.so failed")
         os.replace(tmp, LIB)
-    if force or _stale(BIND, [BIND_SRC, os.path.join(INCLUDE, "hga.h")]):
+    if force or _bind_stale():
         _build_bind()
     return LIB
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def built_for() -> str:
+    """The versions whose objects the binding reads: torch's and Python's."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        version = re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
+    return f"torch {version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _bind_stale() -> bool:
+    if _stale(BIND, [BIND_SRC, os.path.join(INCLUDE, "hga.h")]) or not os.path.exists(BIND_FOR):
+        return True
+    with open(BIND_FOR) as f:
+        return f.read() != built_for()
+
+
 def _build_bind() -> None:
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     tmp = BIND + f".tmp{os.getpid()}"
     inc = os.path.join(torch_dir, "include")
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
+           f'-DHGA_BUILT_FOR="{built_for()}"', f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
            "-isystem" + os.path.join(inc, "torch", "csrc", "api", "include"), BIND_SRC, "-o", tmp,
            f"-L{PKG}", "-l:libhga.so", "-Wl,-rpath,$ORIGIN",
            "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
@@ -103,6 +124,8 @@ def _build_bind() -> None:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         raise RuntimeError("build of _hga_bind.so failed")
     os.replace(tmp, BIND)
+    with open(BIND_FOR, "w") as f:
+        f.write(built_for())
 
 
 if __name__ == "__main__":

@@ -177,4 +177,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_hga_bind", nullptr, -1, g_metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__hga_bind(void) { return PyModule_Create(&g_module); }
+// built_for: the versions of torch and Python whose headers this was compiled with.
+PyMODINIT_FUNC PyInit__hga_bind(void) {
+    PyObject* m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", HGA_BUILT_FOR) != 0) Py_CLEAR(m);
+    return m;
+}

@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import sysconfig
 from typing import Optional
 
 import torch
@@ -211,6 +212,18 @@ try:
 except ImportError as e:
     raise ImportError(f"_hga_bind.so cannot be loaded ({e}): build the library first "
                       "(python -m long_context_rope_b200.build)") from e
+
+
+def _check_built_for(bind) -> None:
+    """The binding reads torch's objects by the layout of the version it was built for."""
+    here = f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+    built = getattr(bind, "built_for", "an unknown version")
+    if built != here:
+        raise ImportError(f"_hga_bind.so was built for {built}, not for {here}: build the library "
+                          "again (python -m long_context_rope_b200.build)")
+
+
+_check_built_for(_bind)
 
 
 def library() -> ctypes.CDLL:
