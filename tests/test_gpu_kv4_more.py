@@ -1,5 +1,7 @@
 """More of the 4-bit store, its attention and rotary positions with several axes on a
 GPU: calls that the documentation allows, each against kv4_ref.py or a longer call."""
+import math
+
 import pytest
 import torch
 
@@ -81,3 +83,199 @@ def test_load_rounds_once(scale):
     assert torch.equal(torch.signbit(got[~nan]), torch.signbit(want[~nan]))
     v = v.cpu().double()
     assert torch.equal(v[~nan], R.values(pages, 1.0)[~nan])
+
+
+# ------------------------------------------- the prefill kernel on the tensor cores
+# Spans of more than 592 units (tokens x sequences x KV heads) of at most 8 heads a KV head, and any of
+# more heads: what the kernel of single tokens does not take.
+def _tc(cfg):
+    assert (cfg.n_q_heads // cfg.n_kv_heads > 8
+            or cfg.q_len * cfg.batch * cfg.n_kv_heads > 592), "not the prefill kernel's"
+    return cfg
+
+
+TC = [(639, 1, 16), (512, 128, 16), (560, 33, 16), (575, 3, 12), (0, 640, 8), (30, 605, 3)]
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed", "late"])
+@pytest.mark.parametrize("q_begin,q_len,heads", TC)
+def test_prefill_scores_that_rise(order, q_begin, q_len, heads):
+    """Keys whose scores grow by orders of magnitude from tile to tile, for some heads only:
+    weights against the first tile's maximum would pass fp16's range, so it is raised and what
+    was summed shrinks. late: the routed groups, which come after the near chunks."""
+    from long_context_rope_b200 import hga
+    cfg = _tc(_cfg4(hga, seq_len=640, q_begin=q_begin, q_len=q_len, n_q_heads=heads,
+                    n_sink=0 if order == "late" else 1, n_local=1, top_k_groups=24, k_scale=2.0 ** -4))
+    k = _rows((1, 1, 640, 128), 130).float()
+    size = torch.arange(640) / 16
+    size = {"rising": size, "falling": 40 - size, "mixed": (size * 7) % 40,
+            "late": size * (torch.arange(640) < 512)}[order].floor()
+    k *= (1 + size)[:, None] ** 1.5
+    q = _rows((1, q_len, heads, 128), 131)
+    q[:, :, :heads // 3] *= 0.01
+    kp = R.pack(*R.quantise(k.to(BF), cfg.k_scale))
+    vp = R.pack(*R.quantise(_rows((1, 1, 640, 128), 132), cfg.v_scale))
+    sel, n = R.lists(cfg, 1, 133)
+    kv = R.values(kp, cfg.k_scale), R.values(vp, cfg.v_scale)
+    if order == "late" and q_begin + q_len == 640:
+        # the last row, tile by tile: its largest weight against its first tile's maximum
+        at = R.visible(cfg, torch.empty(0, dtype=torch.int32), 0, 639)
+        far = torch.cat([torch.arange(16 * g, 16 * g + 16) for g in sel[0, 0, -1, :n[0, 0, -1]].tolist()])
+        s = kv[0][0, 0] @ q[0, -1, -1].double() / 128 ** 0.5 / math.log(2)
+        assert float(s[far].max() - s[at].max()) > 13, "no raise after the first tile"
+    want, tol = R.attend(cfg, q, *kv, sel, n)
+    out = torch.full(q.shape, float("nan"), dtype=BF, device="cuda")
+    hga.attend(cfg, q.cuda(), kp.cuda(), vp.cuda(), sel.cuda(), n.cuda(), out)
+    _clean(hga)
+    _check(out, want, tol)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("q_begin,q_len,heads", [(199, 1, 16), (128, 40, 16), (150, 30, 9), (30, 600, 8)])
+def test_prefill_nan_row(which, q_begin, q_len, heads):
+    """A row with a NaN scale reaches the queries that see it, and no other."""
+    from long_context_rope_b200 import hga
+    long = q_len > 100
+    cfg = _tc(_cfg4(hga, seq_len=640 if long else 256, q_begin=q_begin, q_len=q_len, n_q_heads=heads,
+                    n_local=0, n_sink=0))
+    q, kp, vp, sel, n, want, tol = _attend_case(hga, cfg, 30, count=0)
+    for bad in ([q_begin + q_len // 2] if not long else [70, 127, 128, 333]):
+        p = (kp if which == "k" else vp).clone()
+        p[0, 0, bad // 16, 1024 + (bad % 16) * 8 + 3] = 0x7F
+        out = torch.empty_like(q).cuda()
+        pair = (p, vp) if which == "k" else (kp, p)
+        hga.attend(cfg, q.cuda(), pair[0].cuda(), pair[1].cuda(), sel.cuda(), n.cuda(), out)
+        _clean(hga)
+        at = q_begin + torch.arange(q_len)
+        seen = (at >= bad) & (at // 64 == bad // 64)   # no lists: a query's own chunk alone
+        got = out.cpu().double()
+        assert bool(seen.any()) and torch.isnan(got[0, seen][..., 48:64]).all()
+        assert bool(((got - want).abs()[0, ~seen] <= tol[0, ~seen]).all())
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_begin,q_len,heads", [(199, 1, 16), (64, 140, 16), (150, 30, 11), (0, 610, 8)])
+def test_prefill_nan_query(value, q_begin, q_len, heads):
+    """A query with a NaN or an infinity makes its own row NaN, and no other."""
+    from long_context_rope_b200 import hga
+    cfg = _tc(_cfg4(hga, seq_len=620, q_begin=q_begin, q_len=q_len, n_q_heads=heads))
+    q, kp, vp, sel, n, want, tol = _attend_case(hga, cfg, 30)
+    t, h = q_len // 2, heads - 1
+    q[0, t, h, 5] = value
+    q[0, t, h, 6] = -value
+    out = torch.empty_like(q).cuda()
+    hga.attend(cfg, q.cuda(), kp.cuda(), vp.cuda(), sel.cuda(), n.cuda(), out)
+    _clean(hga)
+    got = out.cpu().double()
+    assert torch.isnan(got[0, t, h]).all()
+    got[0, t, h] = want[0, t, h]
+    _check(got, want, tol)
+
+
+@pytest.mark.parametrize("kw", [dict(q_begin=511, n_q_heads=16), dict(q_begin=448, q_len=64, n_q_heads=16),
+                                dict(q_begin=449, q_len=63, batch=10)])
+def test_prefill_bad_lists_and_counts(kw):
+    """An invalid entry is left out and reported; a count past its list is cut and reported;
+    the rest of the unit, and the other units, stand."""
+    from long_context_rope_b200 import hga
+    cfg = _tc(_cfg4(hga, seq_len=512, **kw))
+    q, kp, vp, sel, n, _, _ = _attend_case(hga, cfg, 50, count=6)
+    kv = [torch.nan_to_num(R.values(p, ts)) for p, ts in ((kp, cfg.k_scale), (vp, cfg.v_scale))]
+
+    def run(sel, n, good):
+        want, tol = R.attend(cfg, q, kv[0], kv[1], sel, good)
+        out = torch.empty_like(q).cuda()
+        hga.attend(cfg, q.cuda(), kp.cuda(), vp.cuda(), sel.cuda(), n.cuda(), out)
+        torch.cuda.synchronize()
+        code = hga.get_device_error()
+        assert hga.get_device_error() == 0
+        _check(out, want, tol)
+        return code
+    assert run(sel, n, n) == 0
+    bad, good = sel.clone(), n.clone()
+    bad[0, 0, 0, 5] = 4 * 7 + 1   # of the current chunk
+    good[0, 0, 0] = 5
+    assert run(bad, n, good) == 2
+    full, cnt = R.lists(cfg, 1, 50)   # every entry of the list is good, the count is not
+    assert int(cnt[0, 0, 0]) == cfg.top_k_groups
+    wrong = cnt.clone()
+    wrong[0, 0, 0] = cfg.top_k_groups + 1
+    assert run(full, wrong, cnt) == 3
+    wrong[0, 0, 0] = -1
+    good = cnt.clone()
+    good[0, 0, 0] = 0
+    assert run(full, wrong, good) == 3
+
+
+@pytest.mark.parametrize("kw", [dict(seq_len=640, q_len=640), dict(seq_len=512, q_len=512, n_q_heads=16)])
+def test_prefill_waits_that_run_out(kw):
+    """Waits that may last a nanosecond (a tile's products, a tile's weights) run out: the launch
+    says so and ends, and the same launch afterwards is as before, bit by bit."""
+    from long_context_rope_b200 import hga
+    cfg = _tc(_cfg4(hga, **kw))
+    c = _attend_case(hga, cfg, 110)
+    args = [t.cuda() for t in c[:5]]
+    first, out = torch.empty_like(args[0]), torch.empty_like(args[0])
+    hga.attend(cfg, *args, first)
+    _clean(hga)
+    _check(first, c[5], c[6])
+    hga.set_wait_limit_ns(1)
+    try:
+        hga.attend(cfg, *args, out)
+        torch.cuda.synchronize()
+        assert hga.get_device_error() == 4
+    finally:
+        hga.set_wait_limit_ns(0)
+    hga.attend(cfg, *args, out)
+    _clean(hga)
+    assert torch.equal(out, first)
+
+
+def test_prefill_streams_and_graphs():
+    """Two prefills at once on two streams, and one captured and replayed on new inputs."""
+    from long_context_rope_b200 import hga
+    cfg = _tc(_cfg4(hga, seq_len=700, q_begin=380, q_len=320, batch=2, n_q_heads=8))
+    cases = [_attend_case(hga, cfg, s) for s in (140, 141)]
+    args = [[t.cuda() for t in c[:5]] for c in cases]
+    outs = [torch.full(c[0].shape, float("nan"), dtype=BF, device="cuda") for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, o, st in zip(args, outs, streams):
+            hga.attend(cfg, *a, o, stream=st)
+    _clean(hga)
+    for c, o in zip(cases, outs):
+        _check(o, c[5], c[6])
+    g = torch.cuda.CUDAGraph()
+    buf, out = [t.clone() for t in args[0]], torch.empty_like(outs[0])
+    with torch.cuda.graph(g):
+        hga.attend(cfg, *buf, out)
+    for a, o in zip(args, outs):
+        for dst, src in zip(buf, a):
+            dst.copy_(src)
+        g.replay()
+        _clean(hga)
+        assert torch.equal(out, o)
+
+
+def test_prefill_offsets_past_32_bits():
+    """Over a store of 4.8 GB per tensor as over a short one."""
+    from long_context_rope_b200 import hga
+    L, n, T = 1 << 20, 512, 16
+    cfg = _tc(_cfg4(hga, batch=8, n_kv_heads=8, n_q_heads=16, seq_len=L, q_begin=L - T, q_len=T, n_sink=0))
+    short = _tc(cfg.copy(seq_len=n, q_begin=n - T))
+    k, v = _rows((8, 8, n, 128), 120).cuda(), _rows((8, 8, n, 128), 121).cuda()
+    q = _rows((8, T, 16, 128), 122).cuda()
+    sel, cnt = R.lists(short, 8, 123)
+    outs = []
+    for c in (cfg, short):
+        shift = c.seq_len - n
+        ks = torch.zeros(c.kv_rows(8, 8, rows=c.seq_len), dtype=torch.uint8, device="cuda")
+        vs, out = torch.zeros_like(ks), torch.empty_like(q)
+        hga.store_kv(c, k, v, ks, vs, shift)
+        moved = torch.where(sel >= 0, sel + shift // 16, sel).cuda()
+        hga.attend(c, q, ks, vs, moved, cnt.cuda(), out)
+        _clean(hga)
+        outs.append(out)
+        del ks, vs
+    assert torch.equal(*outs) and bool(torch.isfinite(outs[0].float()).all())
