@@ -279,3 +279,101 @@ def test_prefill_offsets_past_32_bits():
         outs.append(out)
         del ks, vs
     assert torch.equal(*outs) and bool(torch.isfinite(outs[0].float()).all())
+
+
+# ------------------------------------------------------------------ positions
+SUMS = [("bf16", 128, 20), ("f32", 64, 0), ("f32", 128, 64), ("bf16", 64, 7), ("bf16", 128, 0), ("f32", 128, 33)]
+
+
+@pytest.mark.parametrize("dtype,d,F", SUMS)
+@pytest.mark.parametrize("tables", ["f32", "bf16"])
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("B,H,L,C,every", [(1, 1, 1, 64, False), (2, 3, 200, 64, True), (1, 9, 129, 128, False),
+                                           (2, 1, 96, 32, True), (1, 2, 100, 48, False)])
+def test_summaries_axes_tables(dtype, d, F, tables, rotated, B, H, L, C, every):
+    """Tables of fp32 and bf16, with and without the rotated keys, against the definition; pairs on
+    no axis are plain means. Rows of chunks outside the call stay as they were."""
+    from long_context_rope_b200 import hga, pipeline
+    if (d // 2 // (8 if dtype == "bf16" else 4)) * 4 * (C // 16) % 32:
+        pytest.skip("the framework's configurations do not have this one")
+    cfg = _cfg(hga, batch=B, n_kv_heads=H, n_q_heads=H, seq_len=L, head_dim=d, dtype=dtype,
+               n_high_freq_pairs=min(F, d // 2), chunk_size=C, groups_per_chunk=C // 16,
+               summary_type=int(tables == "bf16"))
+    g = torch.Generator().manual_seed(19)
+    k = torch.randn(B, H, L, d, generator=g).to(cfg.torch_dtype())
+    pair = hga.pair_axes(d // 2, (d // 4, d // 8, d // 8) if every else (d // 8, d // 8, d // 8), True)
+    pos = torch.randint(-1000, 100000, (3, B, L), generator=g, dtype=torch.int32)
+    cs, gs = pipeline.alloc_summaries(cfg)
+    cs.fill_(7.0), gs.fill_(7.0)
+    rot = torch.full_like(k, 7.0).cuda() if rotated else None
+    c0 = 1 if L > C else 0
+    pipeline.summaries(cfg, k.cuda(), cs, gs, rot, axes=hga.rope_axes(pair, 3), positions=pos.cuda(),
+                       chunk_begin=c0)
+    _clean(hga)
+    turned = R.rotate(k, R.angles(pos, pair, 1e4, d)[:, None])
+    mag = (k.double().abs()[..., :d // 2] + k.double().abs()[..., d // 2:]).repeat(1, 1, 1, 2)
+    u = R.BF16 if dtype == "bf16" else R.F32
+    if rotated:
+        assert bool((rot[:, :, :c0 * C] == 7.0).all())
+        err = (rot.cpu().double() - turned).abs()[:, :, c0 * C:]
+        # the sine and cosine are off by 2^-23, product and sum round in fp32
+        assert bool((err <= (mag * (2.0 ** -23 + 3 * R.F32) + u * turned.abs())[:, :, c0 * C:]).all())
+    high = (torch.arange(d) % (d // 2)) < cfg.n_high_freq_pairs
+    for table, size in ((cs, C), (gs, 16)):
+        got, first = table.cpu().double(), c0 * C // size
+        assert bool((got[:, :, :first] == 7.0).all())
+        for i in range(first, table.shape[2]):
+            s = slice(i * size, min(L, (i + 1) * size))
+            if s.start >= L:
+                assert not got[:, :, i].any()
+                continue
+            low = R.rotate(k[:, :, s].double().mean(2, keepdim=True),
+                           R.angles(pos[:, :, s].double().mean(2, keepdim=True), pair, 1e4, d)[:, None])
+            ref = torch.where(high, turned[:, :, s].mean(2), low[:, :, 0])
+            # a sum of at most 128 terms in fp32 and its division, the rotation of the terms or of
+            # the mean, and the table's own rounding
+            e = mag[:, :, s].mean(2) * (2.0 ** -23 + (130 + 3) * R.F32)
+            tol = e + (R.BF16 * (ref.abs() + e) if tables == "bf16" else 0) + 1e-30
+            assert bool(((got[:, :, i] - ref).abs() <= tol).all()), (size, i)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_axes_sine_and_cosine(d, inverse):
+    """Rows of (1, 0) pairs turn into the cosine and the sine themselves. The reduced angle's are off
+    by 2^-23 at most (polynomials in fp32: the last rounding 2^-25, the terms' 2^-25, the series' end
+    2^-29). The angle is a 64-bit product of a 64-bit power: 2^-50 of it covers its roundings here
+    and in the reference."""
+    from long_context_rope_b200 import hga
+    cfg = _cfg(hga, head_dim=d, dtype="f32", rope_theta=5e5)
+    T = 40000
+    g = torch.Generator().manual_seed(21)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (2, 1, T), generator=g)
+    for i, top in enumerate((2, 100, 5000, 70000, 1 << 20)):   # far positions are a sixth only
+        pos[:, :, i::6] %= top
+    pos[:, :, :12] = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 3, 22, 355, 710, 52174, 103993, -355])
+    pos = pos.to(torch.int32)
+    pair = hga.pair_axes(d // 2, (d // 4, d // 4), True)
+    x = torch.zeros(1, T, 1, d)
+    x[..., :d // 2] = 1.0
+    y = torch.empty_like(x).cuda()
+    hga.apply_rope_axes(cfg, hga.rope_axes(pair, 2, inverse=inverse), pos.cuda(), x.cuda(), y, 1, T, 1)
+    _clean(hga)
+    a = R.angles(pos, pair, 5e5, d)
+    want = torch.cat((torch.cos(a), torch.sin(-a if inverse else a)), -1)
+    tol = 2.0 ** -23 + a.abs().repeat(1, 1, 2) * 2.0 ** -50
+    err = (y.cpu().double()[:, :, 0] - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_tensor_of_another_gpu_is_refused():
+    from long_context_rope_b200 import hga
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU here (test_kv4_pipeline_cpu.py has the check itself)")
+    cfg = _cfg4(hga, seq_len=16, q_begin=15)
+    k = torch.zeros(1, 1, 16, 128, dtype=BF, device="cuda:0")
+    st = torch.zeros(1, 1, 1, 1152, dtype=torch.uint8, device="cuda:0")
+    with pytest.raises(ValueError, match="current device"):
+        hga.store_kv(cfg, k.to("cuda:1"), k, st, st, 0)
+    with torch.cuda.device(1), pytest.raises(ValueError, match="current device"):
+        hga.store_kv(cfg, k, k, st, st, 0)

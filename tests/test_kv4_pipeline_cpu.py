@@ -70,3 +70,22 @@ def test_prefill_positions_from_any_token_on(hga, monkeypatch):
     pipeline.prefill(cfg, None, None, None, None, None, None, rb, None, v_store=None,
                      axes=hga.rope_axes([0] * 64, 1), positions=pos)
     assert len(got) == 2 and all(p.data_ptr() % 16 == 0 and torch.equal(p, pos) for p in got)
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_tensor_of_another_device_is_refused(hga, monkeypatch, current):
+    """By its device's number, with a tensor that says it is of a GPU."""
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 1)
+
+        def get_device(self):
+            return 1
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+    t = torch.zeros(4).as_subclass(OnGpu)
+    if current == 1:
+        assert hga._ptr_checked(t, "x", torch.float32, (4,)) == t.data_ptr()
+        return
+    for f in (hga._ptr, hga._ptr_checked):   # the native check passes it on to the other
+        with pytest.raises(ValueError, match="x must be on the current device, cuda:0, not on cuda:1"):
+            f(t, "x", torch.float32, (4,))
