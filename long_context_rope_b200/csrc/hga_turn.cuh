@@ -6,9 +6,10 @@
 
 namespace hga {
 
-// The angle position * inv_freq (a double product) less n quarter turns: pi/2
-// in two parts and fused multiply-adds, so the rest r, |r| <= pi/4, is good to
-// 2^-52 for any int32 position. Returns n's low bits.
+// The angle position * inv_freq as a double product less n quarter turns: pi/2
+// in two parts and fused multiply-adds, so the rest r, |r| <= pi/4, of that product
+// is good to 2^-52 for any int32 position. (The product's own rounding is 2^-53 of
+// the angle: 2^-22 near 2^31, 2^-37 at 2^16.) Returns n's low bits.
 __device__ __forceinline__ int quarter_turns(double position, double inv_freq, double& r) {
     constexpr double kTwoOverPi = 0.63661977236758134308;
     constexpr double kPio2 = 1.57079632679489661923;          // nearest double
@@ -29,9 +30,10 @@ __device__ __forceinline__ void by_quadrant(int q, F cr, F sr, F& c, F& s) {
     s = (q & 2) ? -s0 : s0;
 }
 
-// cos / sin of position * inv_freq, each off by about one fp32 rounding
-// (2^-23.8 measured over the interval, before the rounding of r itself, whose
-// rest is carried along). The Taylor series to r^9 and r^10; the next terms are
+// cos / sin of position * inv_freq, each off by about one fp32 rounding of what the
+// reduced angle has (2^-23.8 measured over the interval, before the rounding of r
+// itself, whose rest is carried along); the product's rounding, above, comes on top
+// at far positions. The Taylor series to r^9 and r^10; the next terms are
 // below 2^-28. The fast rope_cs (2^-21.4) reduces to half a turn and takes the
 // hardware's sine.
 __device__ __forceinline__ void turn_cs(double position, double inv_freq, float& c, float& s) {
@@ -52,7 +54,7 @@ __device__ __forceinline__ void turn_cs(double position, double inv_freq, float&
 }
 
 // The same in 64 bits: Taylor series to r^13 and r^12, off by 2^-41 at most
-// (r^14 / 14!), far below what moves a 4-bit code.
+// (r^14 / 14!) of what the reduced angle has, far below what moves a 4-bit code.
 __device__ __forceinline__ void turn_cs64(double position, double inv_freq, double& c, double& s) {
     double x;
     const int q = quarter_turns(position, inv_freq, x);
