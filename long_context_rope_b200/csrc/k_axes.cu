@@ -422,13 +422,17 @@ cudaError_t launch_rope_axes(const Params& p, const AxisMap& am, const int32_t* 
     sh.lanes_log2 = sh.rlanes_log2 = 0;
     while ((1 << sh.lanes_log2) < lanes) ++sh.lanes_log2;
     const int64_t rows = sh.rep * n_heads;
-    // Row lanes: up to 8 while each has a batch of rows or the grid is short of two
-    // CTAs per SM, more only while there are fewer sites than a CTA would then take.
-    // (2 x 20000 tokens of 4 rows: 26.7 us with a batch a thread, 47.2 with a row.)
+    // Row lanes: up to 8 while each has a batch of rows, or two of them where one would
+    // have more than a batch, or while the grid is short of two CTAs per SM; more than 8
+    // only while there are fewer sites than a CTA would then take. (2 x 20000 tokens of 4
+    // rows: 26.7 us with a batch a thread, 47.2 with a row. 6 and 7 rows in two lanes: 3 x
+    // 4999 x 6 of d = 64 in fp32 11.7 us against 13.1, 2 x 9001 x 7 18.3 against 22.5; the
+    // worst 65536 x 6 of d = 64 in fp32, 42.0 against 40.9.)
     auto more_lanes = [&] {
         const int64_t per_cta = (int64_t)1 << (8 - sh.lanes_log2 - sh.rlanes_log2);
         if (sh.rlanes_log2 >= 3) return per_cta > sh.n_sites;
-        return (int64_t)(2 << sh.rlanes_log2) * kBatch <= rows || sh.n_sites < 2 * 148 * per_cta;
+        return (int64_t)(2 << sh.rlanes_log2) * kBatch <= rows ||
+               (sh.rlanes_log2 == 0 && rows > kBatch) || sh.n_sites < 2 * 148 * per_cta;
     };
     while (sh.lanes_log2 + sh.rlanes_log2 < 8 && (2 << sh.rlanes_log2) <= rows && more_lanes())
         ++sh.rlanes_log2;
@@ -440,7 +444,7 @@ cudaError_t launch_rope_axes(const Params& p, const AxisMap& am, const int32_t* 
     }
     const int sites_log2 = 8 - sh.lanes_log2 - sh.rlanes_log2;
     const int64_t bx = (sh.n_sites + (1 << sites_log2) - 1) >> sites_log2;
-    // Rows per CTA: one batch while the grid is short of two CTAs per SM (the
+    // Rows per CTA: one a lane while the grid is short of two CTAs per SM (the
     // angles are made again, the call's latency counts), more up to all of a
     // site's rows once it fills the GPU.
     int64_t per = (int64_t)1 << sh.rlanes_log2;
