@@ -32,7 +32,9 @@
  *     not allowed while the stream is being captured into a CUDA graph).
  *   - Arguments are validated on the host before anything is launched; a call
  *     that returns an error has launched nothing. Every data pointer must be
- *     16-byte aligned.
+ *     16-byte aligned. A batch with more (sequence, head) units than a launch's
+ *     grid takes (65535) is refused by CUDA: HGA_ERR_CUDA, and later calls are
+ *     not affected.
  *   - Index lists produced by the library are device-side and never copied to
  *     the host. Kernels that read a caller-supplied list check every entry;
  *     an entry out of range, an entry naming a forced chunk, or a list that is

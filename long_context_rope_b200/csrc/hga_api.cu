@@ -166,6 +166,7 @@ hga_status make_params(const hga_config* c, Params* p) {
 thread_local int g_last_cuda_error = 0;
 
 hga_status cuda_failed(cudaError_t e) {
+    cudaGetLastError();  // reported here; the next launch must not find it and report it again
     g_last_cuda_error = (int)e;
     return HGA_ERR_CUDA;
 }

@@ -377,3 +377,35 @@ def test_tensor_of_another_gpu_is_refused():
         hga.store_kv(cfg, k.to("cuda:1"), k, st, st, 0)
     with torch.cuda.device(1), pytest.raises(ValueError, match="current device"):
         hga.store_kv(cfg, k, k, st, st, 0)
+
+
+# ------------------------------------------------------------------- refusals
+@pytest.mark.parametrize("kv4", [False, True])
+def test_launch_that_cuda_refuses_leaves_nothing_behind(kv4):
+    """More units than a grid takes: an error of that call alone, not of the next one, the
+    library's or torch's."""
+    from long_context_rope_b200 import hga
+    kw = dict(batch=70000, n_q_heads=1, seq_len=16, q_begin=15, top_k_groups=1, top_k_chunks=1)
+    cfg = _cfg4(hga, **kw) if kv4 else _cfg(hga, **kw)
+    q = torch.zeros(70000, 1, 1, 128, dtype=BF, device="cuda")
+    st = torch.zeros(cfg.kv_rows(70000, 1, rows=16), dtype=cfg.kv_torch_dtype(), device="cuda")
+    sel = torch.zeros(70000, 1, 1, 1, dtype=torch.int32, device="cuda")
+    small = _cfg4(hga, seq_len=16)
+    pages = torch.zeros(1, 1, 1, 1152, dtype=torch.uint8, device="cuda")
+    k = torch.full((1, 1, 16, 128), 7.0, dtype=BF, device="cuda")
+    torch.cuda.synchronize()
+    with pytest.raises(hga.HgaError, match="HGA_ERR_CUDA"):
+        hga.attend(cfg, q, st, st, sel, sel[..., 0], torch.empty_like(q))
+    hga.load_kv(small, pages, pages, k, k.clone(), 0)
+    _clean(hga)
+    assert not k.any()
+    # what does not put its units on a grid axis takes them all
+    if kv4:
+        rows = torch.randn(70000, 1, 16, 128, device="cuda").to(BF)
+        ks, vs = torch.zeros_like(st), torch.zeros_like(st)
+        hga.store_kv(cfg, rows, rows, ks, vs, 0)
+        one = cfg.copy(batch=1)
+        k1, v1 = ks[:1].clone().zero_(), vs[:1].clone().zero_()
+        hga.store_kv(one, rows[-1:].clone(), rows[-1:].clone(), k1, v1, 0)
+        _clean(hga)
+        assert torch.equal(ks[-1:], k1) and not torch.equal(ks[0], ks[-1])
