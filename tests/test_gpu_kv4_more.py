@@ -409,3 +409,76 @@ def test_launch_that_cuda_refuses_leaves_nothing_behind(kv4):
         hga.store_kv(one, rows[-1:].clone(), rows[-1:].clone(), k1, v1, 0)
         _clean(hga)
         assert torch.equal(ks[-1:], k1) and not torch.equal(ks[0], ks[-1])
+
+
+# --------------------------------------------------------- more shapes and gathers
+TC_SHAPES = [
+    dict(seq_len=200, q_begin=160, q_len=40, chunk_size=16, groups_per_chunk=1, n_q_heads=16),
+    dict(seq_len=700, q_begin=37, q_len=650, chunk_size=16, groups_per_chunk=1),
+    dict(seq_len=700, q_begin=20, q_len=640, chunk_size=32, groups_per_chunk=2, n_q_heads=5),
+    dict(seq_len=500, q_begin=300, q_len=200, chunk_size=112, groups_per_chunk=7, n_q_heads=9),
+    dict(seq_len=700, q_begin=37, q_len=600, chunk_size=128, groups_per_chunk=8),
+    dict(seq_len=640, q_begin=0, q_len=640, n_q_heads=1),
+    dict(seq_len=333, q_begin=332, q_len=1, batch=5, n_kv_heads=2, n_q_heads=66),
+    dict(seq_len=300, q_begin=250, q_len=5, batch=3, n_kv_heads=2, n_q_heads=18),
+    dict(seq_len=7000, q_begin=6950, q_len=40, n_q_heads=10, top_k_groups=400, n_local=1),
+    dict(seq_len=130, q_begin=60, q_len=9, batch=70, n_local=0, n_sink=0, n_q_heads=2),
+]
+
+
+@pytest.mark.parametrize("count", [None, 0, 1])
+@pytest.mark.parametrize("kw", TC_SHAPES, ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_prefill_shapes(kw, count):
+    """Every chunk size, one head and many, a list of hundreds, many short sequences."""
+    from long_context_rope_b200 import hga
+    cfg = _tc(_cfg4(hga, **kw))
+    q, kp, vp, sel, n, want, tol = _attend_case(hga, cfg, 150, count)
+    args = [t.cuda() for t in (q, kp, vp, sel, n)]
+    outs = [torch.full(q.shape, float("nan"), dtype=BF, device="cuda") for _ in range(2)]
+    for out in outs:
+        hga.attend(cfg, *args, out)
+    _clean(hga)
+    _check(outs[0], want, tol)
+    assert torch.equal(*outs)
+
+
+def test_gathers_of_pages_for_a_span_and_without_a_buffer():
+    """Pages of several query chunks from host memory as from the device; the warm tier that is
+    given no list buffer, as the one that is."""
+    from long_context_rope_b200 import hga, pipeline
+    cfg = _cfg4(hga, seq_len=999, q_begin=500, q_len=300, batch=2, n_kv_heads=2, n_q_heads=16)
+    g = torch.Generator().manual_seed(160)
+    pages = [torch.randint(0, 256, cfg.kv_rows(2, 2, rows=999), generator=g, dtype=torch.uint8)
+             for _ in "kv"]
+    sel, n = R.lists(cfg, 2, 161)
+    sd, nd = sel.cuda(), n.cuda()
+    host, dev = pipeline.alloc_gathered(cfg), pipeline.alloc_gathered(cfg)
+    pinned = [p.pin_memory() for p in pages]
+    hga.gather_kv(cfg, *pinned, True, sd, nd, *host)
+    hga.gather_kv(cfg, *(p.cuda() for p in pages), False, sd, nd, *dev)
+    _clean(hga)
+    for a, b, p in zip(host, dev, pages):
+        assert torch.equal(a, b)
+        for bb in range(2):
+            for h in range(2):
+                for j in range(cfg.n_qchunks):
+                    m = int(n[bb, h, j])
+                    assert torch.equal(a[bb, h, j, :m].cpu(), p[bb, h, sel[bb, h, j, :m].long()])
+    one = cfg.copy(q_begin=998, q_len=1)
+    pools = [pipeline.alloc_warm_pool(one, 20) for _ in range(2)]
+    for step in range(3):
+        sel, n = R.lists(one, 2, 170 + step)
+        sd, nd = sel.cuda(), n.cuda()
+        outs = [pipeline.alloc_gathered(one) for _ in range(2)]
+        for pool, out, free in zip(pools, outs, (False, True)):
+            head = (one, *pinned, sd, nd, pool.k, pool.v, pool.tag, pool.last, step)
+            if free:
+                hga.gather_kv_warm_noalloc(*head, *out, pool.stats)
+            else:
+                hga.gather_kv_warm(*head, pool.src, *out, pool.stats)
+        _clean(hga)
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        for name in ("k", "v", "tag", "last", "stats"):
+            assert torch.equal(getattr(pools[0], name), getattr(pools[1], name))
+        m = int(n[1, 1, 0])
+        assert torch.equal(outs[0][0][1, 1, 0, :m].cpu(), pages[0][1, 1, sel[1, 1, 0, :m].long()])
