@@ -482,3 +482,26 @@ def test_gathers_of_pages_for_a_span_and_without_a_buffer():
             assert torch.equal(getattr(pools[0], name), getattr(pools[1], name))
         m = int(n[1, 1, 0])
         assert torch.equal(outs[0][0][1, 1, 0, :m].cpu(), pages[0][1, 1, sel[1, 1, 0, :m].long()])
+
+
+@pytest.mark.parametrize("q_len,heads,gathered", [(1, 12, False), (30, 12, False), (1, 130, False), (1, 12, True)])
+def test_attend_large_queries(q_len, heads, gathered):
+    """Queries beyond the range of 16-bit floats with 5 exponent bits, and tiny ones, on the
+    kernels that take more heads than single tokens' does."""
+    from long_context_rope_b200 import hga, pipeline
+    cfg = _cfg4(hga, seq_len=400, q_begin=400 - q_len, q_len=q_len, k_scale=2.0 ** -30, n_q_heads=heads)
+    kp = R.pack(*R.quantise(_rows((1, 1, 400, 128), 1, 2.0 ** -22), cfg.k_scale))
+    vp = R.pack(*R.quantise(_rows((1, 1, 400, 128), 2), cfg.v_scale))
+    q = _rows((1, q_len, heads, 128), 3)
+    q *= torch.tensor([2.0 ** 20, 2.0 ** 22, 1.0, 2.0 ** -20])[torch.arange(heads) % 4].view(1, 1, -1, 1).to(BF)
+    sel, n = R.lists(cfg, 1, 0)
+    want, tol = R.attend(cfg, q, R.values(kp, cfg.k_scale), R.values(vp, cfg.v_scale), sel, n)
+    args = [t.cuda() for t in (q, kp, vp, sel, n)]
+    gat = (None, None)
+    if gathered:
+        gat = pipeline.alloc_gathered(cfg)
+        hga.gather_kv(cfg, args[1], args[2], False, args[3], args[4], *gat)
+    out = torch.empty_like(args[0])
+    hga.attend(cfg, *args, out, k_gat=gat[0], v_gat=gat[1])
+    _clean(hga)
+    _check(out, want, tol)
