@@ -282,8 +282,10 @@ bool decode_kernel_supports(const Params& p) {
     // A span over a 4-bit store token by token, while a CTA of every token's unit is
     // resident (four an SM): the prefill kernel's few units would leave most SMs idle,
     // each with its tiles one after another. 48 tokens of one KV head, 36 key blocks:
-    // 8.5 against 21.8 us; 64 and 148 tokens of four, 130: 27.3 and 45.4 against 49.5;
-    // 592 of one, 76: 29.3 against 35.1.
+    // 8.4 against 21.8 us; 64 and 148 tokens of four, 130: 27.1 and 45.3 against 49.5;
+    // 592 of one, 76: 29.2 against 35.1. That is one sequence. Few tokens each of many
+    // would gain past the limit too: four of 37 sequences x four KV heads take 38 us here,
+    // and of 38, which go to the prefill kernel, 76.
     if (p.kv_f4)
         return p.q_len == 1 || (p.Hu == p.Hkv && (int64_t)p.q_len * p.B * p.Hkv <= 4 * 148);
     return p.dtype == HGA_BF16 && p.d == kD && p.q_len == 1 && p.L % kGroupRows == 0;

@@ -14,7 +14,7 @@
 // eight warps, two per SM: the same up to 296 units, where all are resident
 // either way; two us more for 512 units of 108 pages, which then take two rounds of
 // CTAs.) Bound by instructions, about 390 a page, at 16 warps an SM: 127 MB in
-// 37 us.
+// 38 us.
 // hga_decode_pages.cuh has the arithmetic and the joining of the partials.
 #include <cooperative_groups.h>
 

@@ -29,8 +29,7 @@
 // Bound by the alternation of products and softmax within a unit (the tensor
 // cores wait while a tile's weights are made; both M tiles in turn hide most of
 // it) and by the start and end of units, 8000 cycles each: 32 heads over 4, the
-// last 16K tokens of 32K in 508 to 527 us (898 to 931 TFLOP/s), 4K tokens in 113
-// to 119 us.
+// last 16K tokens of 32K in 533 us (887 TFLOP/s), 4K tokens in 114 us.
 //
 // Spans of few tokens (at most 8 heads per KV head) go to k_attend_pages.cu.
 //

@@ -24,8 +24,8 @@ namespace {
 // in shared memory. Then a thread owns V pairs of one site in registers and
 // turns rows of it, kBatch rows' loads in flight. Rows of a site: rr = r *
 // n_heads + h, r < rep; thread (site, row lane, pair slice). 64K tokens x 32
-// heads (1.07 GB) in 178 to 186 us, 5.8 to 6 TB/s; one token of 16 sequences x 32
-// heads in 2.9 us.
+// heads (1.07 GB) in 173 us in the same buffers again and again, 188 in others each
+// time (6.2 and 5.7 TB/s); one token of 16 sequences x 32 heads in 3.0 us.
 constexpr int kRopeThreads = 256;
 constexpr int kBatch = 4;
 constexpr int kRopeCtas = 3;
@@ -166,8 +166,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_axes_kernel(
 // go over the groups in order. Mean positions are sums of integers, exact to
 // double rounding. A token's rows of the next head are loaded as soon as the
 // current ones are unpacked. 64K tokens x 4 heads (145 MB with the rotated keys)
-// in 43 us, 3.4 TB/s: the angles of a chunk and the rotation's instructions bound
-// it, not the memory (5 or 6 CTAs an SM, at 96 or 80 registers: 47.5, 60 us).
+// in 43 us, 3.4 TB/s, and 33.5 without them. It waits, with neither the memory nor
+// the issue slots at a limit (47% of those in its profile): first for table reads,
+// shuffles and conversions (short scoreboard), at 16 warps an SM. (5 or 6 CTAs an SM,
+// at 96 or 80 registers: 47.5, 60 us.)
 //
 // In the tables, 16-byte piece j of a row sits at j ^ (j >> 3), so that the
 // eight lanes of a row read different banks.

@@ -10,8 +10,10 @@
 // row and tensor), so what counts is that every access of a warp covers whole
 // sectors, with a few loads in flight per thread, and few instructions per
 // element (a correctly rounded quotient in three). 64K tokens x 4 heads (172
-// MB each way): written in 38 us, bound by instructions; read back in 28.5 us,
-// 0.92 of the copy bandwidth.
+// MB each way): written in 38 us, bound by instructions; read back in 31.5 us,
+// 0.83 of the copy bandwidth (36 under a tensor scale of more than 18 bits, whose
+// products take more instructions to round once). Keys rotated by positions on the
+// way make that 121 us: every KV head makes a token's angles again, in 64 bits.
 #include <string.h>
 
 #include "hga_e2m1.cuh"

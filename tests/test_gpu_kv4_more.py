@@ -173,12 +173,13 @@ def test_prefill_nan_query(value, q_begin, q_len, heads):
 
 
 @pytest.mark.parametrize("kw", [dict(q_begin=511, n_q_heads=16), dict(q_begin=448, q_len=64, n_q_heads=16),
-                                dict(q_begin=449, q_len=63, batch=10)])
-def test_prefill_bad_lists_and_counts(kw):
+                                dict(q_begin=449, q_len=63, batch=10),
+                                dict(q_begin=511), dict(q_begin=480, q_len=4, n_q_heads=3)])  # token by token
+def test_bad_lists_and_counts_by_either_kernel(kw):
     """An invalid entry is left out and reported; a count past its list is cut and reported;
     the rest of the unit, and the other units, stand."""
     from long_context_rope_b200 import hga
-    cfg = _tc(_cfg4(hga, seq_len=512, **kw))
+    cfg = _cfg4(hga, seq_len=512, **kw)
     q, kp, vp, sel, n, _, _ = _attend_case(hga, cfg, 50, count=6)
     kv = [torch.nan_to_num(R.values(p, ts)) for p, ts in ((kp, cfg.k_scale), (vp, cfg.v_scale))]
 
