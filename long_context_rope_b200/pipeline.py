@@ -112,8 +112,8 @@ def _as_stream(stream) -> torch.cuda.Stream:
 def _aligned(positions: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
     """Positions at an address that the calls take. One axis of one sequence from some
     token on is contiguous as it lies, wherever it starts: it is copied, on `stream`."""
-    if positions is None or positions.data_ptr() % 16 == 0:
-        return positions
+    if not isinstance(positions, torch.Tensor) or positions.data_ptr() % 16 == 0:
+        return positions  # None, or for the call's own check
     if stream is None or not positions.is_cuda:
         return positions.clone()
     with torch.cuda.stream(_as_stream(stream)):
